@@ -61,12 +61,14 @@ typedef enum {
     MAXSIM_OK = 0,
     MAXSIM_ERR_NULL = 1,        /* a required pointer is NULL */
     MAXSIM_ERR_SHAPE = 2,       /* a negative size or inconsistent sizes */
-    MAXSIM_ERR_UNSUPPORTED = 3, /* d outside 1..1024, an unknown dtype, a misaligned pointer */
+    MAXSIM_ERR_UNSUPPORTED = 3, /* a width or value out of range, an unknown dtype, a misaligned pointer */
     MAXSIM_ERR_OVERFLOW = 4,    /* an index or an int32 sum could overflow */
     MAXSIM_ERR_LAUNCH = 5       /* the HIP runtime refused a launch */
 } maxsim_status_t;
 
-typedef enum { MAXSIM_F16 = 0, MAXSIM_BF16 = 1 } maxsim_dtype_t;
+/* Embeddings are scored as F16 or BF16; F32 and I8 are types of rows of the
+ * embedding head (maxsim_embed.h) and UNSUPPORTED here. */
+typedef enum { MAXSIM_F16 = 0, MAXSIM_BF16 = 1, MAXSIM_F32 = 2, MAXSIM_I8 = 3 } maxsim_dtype_t;
 
 /*
  * Cross-product forward ("Flash-MaxSim" Sec. 4.1; design notes "Forward",

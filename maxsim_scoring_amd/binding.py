@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libmaxsim_amd.so")
 
 MAXSIM_F16 = 0
 MAXSIM_BF16 = 1
+MAXSIM_F32 = 2
+MAXSIM_I8 = 3
 D_MODEL = 128
 
 _lib = None
@@ -60,6 +62,18 @@ def lib() -> ctypes.CDLL:
         L.maxsim_chamfer_fwd.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp]
         L.maxsim_chamfer_bwd.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                          vp, vp]
+        u64, f64 = ctypes.c_uint64, ctypes.c_double
+        L.maxsim_quantize_tok.argtypes = [ci, vp, i64, i64, vp, ci, vp, vp, vp]
+        L.maxsim_linear_i8.argtypes = [ci, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp]
+        L.maxsim_embed_i8.argtypes = [ci, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
+        L.maxsim_normalize_fwd.argtypes = [ci, vp, i64, i64, vp, ci, vp, vp, vp]
+        L.maxsim_normalize_bwd.argtypes = [ci, vp, vp, vp, i64, i64, ci, vp, vp]
+        L.maxsim_dropout_fwd.argtypes = [ci, vp, i64, f64, u64, u64, vp, vp, vp]
+        L.maxsim_dropout_bwd.argtypes = [ci, vp, i64, f64, u64, u64, vp, vp, vp]
+        for f in (L.maxsim_quantize_tok, L.maxsim_linear_i8, L.maxsim_embed_i8,
+                  L.maxsim_normalize_fwd, L.maxsim_normalize_bwd, L.maxsim_dropout_fwd,
+                  L.maxsim_dropout_bwd):
+            f.restype = ci
         for f in (L.maxsim_fwd, L.maxsim_fwd_varlen, L.maxsim_fwd_i8, L.maxsim_bwd,
                   L.maxsim_fwd_i8_tok, L.maxsim_fwd_pairs, L.maxsim_topk,
                   L.maxsim_fwd_pairs_varlen, L.maxsim_bwd_varlen, L.maxsim_chamfer_fwd,
@@ -522,3 +536,233 @@ def two_stage_topk(Qi8: torch.Tensor, q_scale: torch.Tensor, Di8: torch.Tensor,
                                 stream=stream)
     doc, val, _ = maxsim_topk(exact.view(Nq, candidates), k, ids=cand, stream=stream)
     return doc, val, s8
+
+
+# ---------------------------------------------------------------------------
+# The embedding head (include/maxsim_embed.h): hidden states to token
+# embeddings. Rows may have any leading dimensions ([T, d], [Nd, Ld, d], ...).
+# ---------------------------------------------------------------------------
+
+_ROW_TYPES = {torch.float16: MAXSIM_F16, torch.bfloat16: MAXSIM_BF16, torch.float32: MAXSIM_F32}
+
+
+def _row_type(name: str, dtype) -> int:
+    if dtype not in _ROW_TYPES:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32, got {dtype}")
+    return _ROW_TYPES[dtype]
+
+
+class _On:
+    """The device and stream of one call: the device of its first tensor, and
+    that device's current stream unless one is given. Entered, both are
+    current, so the call launches there and the outputs it allocates belong to
+    that stream."""
+
+    def __init__(self, stream, **tensors):
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            _dev(name, t)
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream must be one of {dev}, got {stream.device}")
+        self.device = dev
+        self._stream = stream
+        self._ctx = None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device() or self._stream is not None:
+            self._ctx = torch.cuda.stream(self._stream if self._stream is not None
+                                          else torch.cuda.current_stream(self.device))
+            self._ctx.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        return False
+
+
+def _rows(name: str, t: torch.Tensor):
+    """(leading shape, rows, width) of a tensor of rows."""
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have rows in its last dimension")
+    lead = tuple(t.shape[:-1])
+    rows = 1
+    for n in lead:
+        rows *= n
+    return lead, rows, t.shape[-1]
+
+
+def maxsim_quantize_tok(X: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                        normalize: bool = False, codes: Optional[torch.Tensor] = None,
+                        scale: Optional[torch.Tensor] = None, stream=None):
+    """Rows X [..., d] fp16/bf16/fp32 to int8 codes and one scale per token, the
+    inputs of maxsim_fwd_i8_tok and maxsim_linear_i8: codes * scale is X, or with
+    ``normalize`` X over its row norms. mask uint8 [...]: masked rows (and rows
+    of zeros) get codes 0, scale 1. Returns (codes int8 [..., d], scale float32 [...])."""
+    code = _row_type("X", X.dtype)
+    lead, T, d = _rows("X", X)
+    _mask("mask", mask, lead)
+    with _On(stream, X=X, mask=mask, codes=codes, scale=scale) as st:
+        if codes is None:
+            codes = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+        if scale is None:
+            scale = torch.empty(lead, dtype=torch.float32, device=X.device)
+        _out("codes", codes, torch.int8, X.shape)
+        _out("scale", scale, torch.float32, lead)
+        _check("maxsim_quantize_tok",
+               lib().maxsim_quantize_tok(code, _p(X), T, d, _p(mask), int(bool(normalize)),
+                                         _p(codes), _p(scale), st))
+    return codes, scale
+
+
+def _linear_args(A, a_scale, W, w_scale, bias):
+    lead, T, K = _rows("A", A)
+    if W.dim() != 2 or W.shape[1] != K:
+        raise ValueError(f"W must be [N, {K}], got {list(W.shape)}")
+    N = W.shape[0]
+    _dev("A", A, torch.int8)
+    _dev("W", W, torch.int8)
+    for name, t, shape in (("a_scale", a_scale, lead), ("w_scale", w_scale, (N,)), ("bias", bias, (N,))):
+        _out(name, t, torch.float32, shape)
+    return lead, T, K, N
+
+
+def maxsim_linear_i8(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
+                     w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                     out_dtype=torch.bfloat16, Y: Optional[torch.Tensor] = None, stream=None):
+    """8-bit product a_scale * w_scale * (A W^T) + bias. A int8 [..., K], a_scale
+    float32 [...], W int8 [N, K], w_scale and bias float32 [N]. Returns Y [..., N]
+    of ``out_dtype`` (fp16, bf16 or fp32)."""
+    lead, T, K, N = _linear_args(A, a_scale, W, w_scale, bias)
+    code = _row_type("out_dtype", out_dtype if Y is None else Y.dtype)
+    with _On(stream, A=A, a_scale=a_scale, W=W, w_scale=w_scale, bias=bias, Y=Y) as st:
+        if Y is None:
+            Y = torch.empty(lead + (N,), dtype=out_dtype, device=A.device)
+        _out("Y", Y, Y.dtype, lead + (N,))
+        _check("maxsim_linear_i8",
+               lib().maxsim_linear_i8(code, _p(A), _p(a_scale), _p(W), _p(w_scale), _p(bias), T, N,
+                                      K, _p(Y), st))
+    return Y
+
+
+def maxsim_embed_i8(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
+                    w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    mask: Optional[torch.Tensor] = None, out_dtype=torch.int8,
+                    E: Optional[torch.Tensor] = None, e_scale: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Token embeddings from 8-bit hidden states: maxsim_linear_i8 with W [d, K],
+    each row over its norm. ``out_dtype`` int8 gives codes and scales for
+    maxsim_fwd_i8_tok, fp16, bf16 or fp32 the embeddings themselves. mask uint8
+    [...]: masked rows give zeros (codes 0, scale 1). Returns (E [..., d],
+    e_scale float32 [...] or None)."""
+    lead, T, K, d = _linear_args(A, a_scale, W, w_scale, bias)
+    _mask("mask", mask, lead)
+    dt = out_dtype if E is None else E.dtype
+    code = MAXSIM_I8 if dt == torch.int8 else _row_type("out_dtype", dt)
+    if code != MAXSIM_I8 and e_scale is not None:
+        raise ValueError("e_scale is an output of int8 embeddings only")
+    with _On(stream, A=A, a_scale=a_scale, W=W, w_scale=w_scale, bias=bias, mask=mask, E=E,
+             e_scale=e_scale) as st:
+        if E is None:
+            E = torch.empty(lead + (d,), dtype=dt, device=A.device)
+        if e_scale is None and code == MAXSIM_I8:
+            e_scale = torch.empty(lead, dtype=torch.float32, device=A.device)
+        _out("E", E, dt, lead + (d,))
+        _out("e_scale", e_scale, torch.float32, lead)
+        _check("maxsim_embed_i8",
+               lib().maxsim_embed_i8(code, _p(A), _p(a_scale), _p(W), _p(w_scale), _p(bias),
+                                     _p(mask), T, d, K, _p(E), _p(e_scale), st))
+    return E, e_scale
+
+
+def embed_tokens_i8(H: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                    out_dtype=torch.int8, stream=None):
+    """Hidden states H [..., K] fp16/bf16/fp32 to token embeddings through an
+    8-bit projection (W int8 [d, K], w_scale [d]): the states are quantised per
+    token, multiplied and normalised. Two library calls. Returns
+    (E [..., d], e_scale [...] or None), as maxsim_embed_i8."""
+    codes, scale = maxsim_quantize_tok(H, mask, stream=stream)
+    return maxsim_embed_i8(codes, scale, W, w_scale, bias, mask, out_dtype=out_dtype, stream=stream)
+
+
+def maxsim_normalize_fwd(X: torch.Tensor, mask: Optional[torch.Tensor] = None, out_dtype=None,
+                         Y: Optional[torch.Tensor] = None, rnorm: Optional[torch.Tensor] = None,
+                         stream=None):
+    """Rows X [..., d] (fp16/bf16/fp32) over their Euclidean norms. mask uint8
+    [...]: masked rows (and rows of zeros) give zeros. Returns (Y [..., d] of
+    ``out_dtype``, X's by default, rnorm float32 [...] = 1/norm)."""
+    xt = _row_type("X", X.dtype)
+    dt = Y.dtype if Y is not None else X.dtype if out_dtype is None else out_dtype
+    yt = _row_type("out_dtype", dt)
+    lead, T, d = _rows("X", X)
+    _mask("mask", mask, lead)
+    with _On(stream, X=X, mask=mask, Y=Y, rnorm=rnorm) as st:
+        if Y is None:
+            Y = torch.empty(X.shape, dtype=dt, device=X.device)
+        if rnorm is None:
+            rnorm = torch.empty(lead, dtype=torch.float32, device=X.device)
+        _out("Y", Y, dt, X.shape)
+        _out("rnorm", rnorm, torch.float32, lead)
+        _check("maxsim_normalize_fwd",
+               lib().maxsim_normalize_fwd(xt, _p(X), T, d, _p(mask), yt, _p(Y), _p(rnorm), st))
+    return Y, rnorm
+
+
+def maxsim_normalize_bwd(X: torch.Tensor, rnorm: torch.Tensor, dY: torch.Tensor, out_dtype=None,
+                         dX: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of maxsim_normalize_fwd: X and rnorm as there, dY float32 [..., d]
+    (the dQ or dD of maxsim_bwd). Returns dX [..., d] of ``out_dtype``, X's by
+    default."""
+    xt = _row_type("X", X.dtype)
+    dt = dX.dtype if dX is not None else X.dtype if out_dtype is None else out_dtype
+    gt = _row_type("out_dtype", dt)
+    lead, T, d = _rows("X", X)
+    with _On(stream, X=X, rnorm=rnorm, dY=dY, dX=dX) as st:
+        _out("rnorm", rnorm, torch.float32, lead)
+        _out("dY", dY, torch.float32, X.shape)
+        if dX is None:
+            dX = torch.empty(X.shape, dtype=dt, device=X.device)
+        _out("dX", dX, dt, X.shape)
+        _check("maxsim_normalize_bwd",
+               lib().maxsim_normalize_bwd(xt, _p(X), _p(rnorm), _p(dY), T, d, gt, _p(dX), st))
+    return dX
+
+
+def _dropout(fn: str, X, p, seed, step, step_dev, Y, stream, names):
+    code = _row_type(names[0], X.dtype)
+    for name, v in (("seed", seed), ("step", step)):
+        if not 0 <= int(v) < 1 << 64:
+            raise ValueError(f"{name} must be in [0, 2^64), got {v}")
+    with _On(stream, **{names[0]: X, "step_dev": step_dev, names[1]: Y}) as st:
+        if step_dev is not None and (step_dev.dtype != torch.int64 or step_dev.numel() != 1):
+            raise ValueError("step_dev must be one int64")
+        if Y is None:
+            Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        _out(names[1], Y, X.dtype, X.shape)
+        _check(fn, getattr(lib(), fn)(code, _p(X), X.numel(), float(p), int(seed), int(step),
+                                      _p(step_dev), _p(Y), st))
+    return Y
+
+
+def maxsim_dropout_fwd(X: torch.Tensor, p: float, seed: int, step: int = 0,
+                       step_dev: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                       stream=None):
+    """Dropout of X (any shape, fp16/bf16/fp32) with probability p, kept elements
+    times 1/(1-p). The mask is a function of (seed, step + step_dev, element) and
+    is not stored; step_dev is one int64 on the GPU, read when the kernel runs.
+    Returns Y."""
+    return _dropout("maxsim_dropout_fwd", X, p, seed, step, step_dev, Y, stream, ("X", "Y"))
+
+
+def maxsim_dropout_bwd(dY: torch.Tensor, p: float, seed: int, step: int = 0,
+                       step_dev: Optional[torch.Tensor] = None, dX: Optional[torch.Tensor] = None,
+                       stream=None):
+    """Gradient of maxsim_dropout_fwd with the same p, seed and step. Returns dX."""
+    return _dropout("maxsim_dropout_bwd", dY, p, seed, step, step_dev, dX, stream, ("dY", "dX"))

@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmaxsim_amd.so")
-SOURCES = ["abi.hip", "fwd_dense.hip", "fwd_varlen.hip", "fwd_dim.hip", "bwd.hip", "topk.hip", "chamfer.hip"]
+SOURCES = ["abi.hip", "fwd_dense.hip", "fwd_varlen.hip", "fwd_dim.hip", "bwd.hip", "topk.hip", "chamfer.hip",
+           "embed_abi.hip", "embed_rows.hip", "embed_linear.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -34,8 +35,12 @@ FLAGS = [
 # Per-source additions. The Chamfer kernel's MFMA results feed VALU min
 # updates directly, so they go to ordinary VGPRs instead of the
 # accumulation registers (no copy back per MFMA); the other kernels keep the
-# compiler's default register form.
-EXTRA = {"chamfer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# compiler's default register form. The embedding head carries activations and
+# gradients, where an overflow upstream must stay visible: NaNs are honoured
+# there (later flags win).
+_NANS = ["-Xarch_device", "-fhonor-nans", "-Xarch_device", "-mamdgpu-ieee"]
+EXTRA = {"chamfer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "embed_rows.hip": _NANS, "embed_linear.hip": _NANS}
 
 
 def _run(cmd, verbose):

@@ -17,7 +17,7 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 constexpr int kD = 128;     // embedding width handled by every kernel
 constexpr int kWave = 64;
 
-enum Elem : int { kF16 = 0, kBF16 = 1, kI8 = 2 };
+enum Elem : int { kF16 = 0, kBF16 = 1, kI8 = 2, kF32 = 3 };
 
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 

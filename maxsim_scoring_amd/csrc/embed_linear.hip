@@ -1,0 +1,624 @@
+// 8-bit matrix product with a scale per token and per output channel, and the
+// same product with every row normalised (and quantised), for gfx950.
+//
+//   y[t,n] = a_scale[t] w_scale[n] sum_k A[t,k] W[n,k] + bias[n]
+//
+// The product runs transposed on the int8 matrix cores, W . A^T: MFMA rows are
+// output channels and columns are tokens, so a lane holds channels of one
+// token. The statistics of a row (its norm and largest magnitude) are then
+// sums and maxima inside a lane, over the lanes that share the token, and over
+// the waves that split the channels.
+//
+// tile_kernel: BT tokens x BN channels per workgroup; A and W tiles of KB bytes
+// along k stream through a ring in LDS by direct-to-LDS loads, with 16-byte
+// chunks swizzled against bank conflicts.
+// few_kernel: a few tokens. W is the traffic; every fragment goes straight from
+// memory to registers, waves split k, and LDS joins their sums.
+#include <type_traits>
+
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace maxsim {
+
+namespace {
+
+constexpr float kTiny = 0x1p-110f;  // rows below this count as zeros
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
+
+__device__ __forceinline__ uint32_t half_bits(int out, float v)
+{
+    return out == kBF16 ? (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v)
+                        : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// 16 bytes of a row of K bytes from byte k on; bytes past the row's end are 0.
+// UNAL: the row may start at any byte address.
+template <bool UNAL>
+__device__ __forceinline__ i32x4 load16(const int8_t* row, int k, int K)
+{
+    if constexpr (!UNAL) {
+        return k < K ? *(const i32x4*)(row + k) : i32x4{};
+    } else {
+        if (k + 16 <= K) {
+            const i32x4_any v = *(const i32x4_any*)(row + k);
+            return i32x4{v[0], v[1], v[2], v[3]};
+        }
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (k + i < K) w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
+        return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    }
+}
+
+// y in float32: the sum, the scales' product and the bias each round once (no
+// fused multiply-add, so the result does not depend on the kernel).
+__device__ __forceinline__ float scaled(int acc, float as, float ws, float b)
+{
+#pragma clang fp contract(off)
+    const float s = as * ws;
+    return (float)acc * s + b;
+}
+__device__ __forceinline__ double scaled64(int acc, double as, float ws, float b)
+{
+    return (double)acc * (as * (double)ws) + (double)b;
+}
+
+// Four consecutive outputs n .. n + 3 of row t. vec: N is a multiple of 4.
+__device__ __forceinline__ void store4(void* Y, int out, int64_t t, int n, int N, bool vec, const float (&y)[4])
+{
+    const int64_t at = t * N + n;
+    if (vec) {
+        if (n >= N) return;
+        if (out == kF32) {
+            *(f32x4*)((float*)Y + at) = f32x4{y[0], y[1], y[2], y[3]};
+        } else {
+            *(u32x2*)((uint16_t*)Y + at) = u32x2{half_bits(out, y[0]) | half_bits(out, y[1]) << 16,
+                                                half_bits(out, y[2]) | half_bits(out, y[3]) << 16};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= N) return;
+        if (out == kF32) ((float*)Y)[at + i] = y[i];
+        else ((uint16_t*)Y)[at + i] = (uint16_t)half_bits(out, y[i]);
+    }
+}
+__device__ __forceinline__ void store4_codes(void* Y, int64_t t, int n, int N, bool vec, const int (&q)[4])
+{
+    int8_t* p = (int8_t*)Y + t * N + n;
+    if (vec) {
+        if (n < N)
+            *(uint32_t*)p = (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 |
+                            (uint32_t)q[3] << 24;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < N) p[i] = (int8_t)q[i];
+}
+
+// f(integral_constant<int, I>) for I = B .. E-1, unrolled at compile time
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for(F&& f)
+{
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        static_for<B + 1, E>(f);
+    }
+}
+
+struct AddF { template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a + b; } };
+struct MaxF {
+    __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_fmaxf(a, b); }
+    __device__ __forceinline__ double operator()(double a, double b) const { return __builtin_fmax(a, b); }
+};
+
+__device__ __forceinline__ float xor_lane(float v, int m) { return shfl_xor_f(v, m); }
+__device__ __forceinline__ double xor_lane(double v, int m) { return __shfl_xor(v, m, 64); }
+
+// Joins one value per token over the lanes that share it (lane / COLS) and over
+// the WN waves that hold other channels, in a fixed order. `red` holds WN rows
+// of `stride` doubles; `slot` is the token's place in a row. Every wave of the
+// workgroup calls it; those that hold no sums pass wn < 0.
+template <int COLS, int WN, typename V, typename OP>
+__device__ __forceinline__ V join_token(V v, OP op, double* red, int stride, int slot, int wn)
+{
+#pragma unroll
+    for (int m = COLS; m < 64; m *= 2) v = op(v, xor_lane(v, m));
+    if constexpr (WN > 1) {
+        __syncthreads();
+        if (wn >= 0 && lane_id() < COLS) red[wn * stride + slot] = (double)v;
+        __syncthreads();
+        v = (V)red[slot];
+#pragma unroll
+        for (int w = 1; w < WN; ++w) v = op(v, (V)red[w * stride + slot]);
+    }
+    return v;
+}
+
+// Normalises the rows that a workgroup holds and writes them. A lane holds, for
+// each of TT tokens, NB groups of 4 consecutive channels: get(tt, b, i) is the
+// int32 sum, chan(b) the first channel of group b. ws and bs (LDS) hold the
+// scales and biases of the workgroup's channels, 0 past the last one.
+template <int TT, int NB, int COLS, int WN, typename GET, typename CHAN>
+__device__ __forceinline__ void embed_rows(const LinearArgs& a, GET get, CHAN chan, const float* ws, const float* bs,
+                                           const int64_t (&t)[TT], const int (&slot)[TT], int wn, double* red,
+                                           int stride)
+{
+    const bool vec = (a.N & 3) == 0;
+    static_for<0, TT>([&](auto tt) {
+        const bool in = t[tt] < a.T;
+        const bool live = in && (!a.mask || a.mask[t[tt]]);
+        const float as = live ? a.a_scale[t[tt]] : 0.0f;
+        if (a.out != kI8) {
+            float top = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = __builtin_fmaxf(top, __builtin_fabsf(scaled(get(tt, b, i), as, w[i], c[i])));
+            }
+            top = join_token<COLS, WN>(live ? top : 0.0f, MaxF{}, red, stride, slot[tt], wn);
+            const float inv = 1.0f / top;
+            float ss = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = scaled(get(tt, b, i), as, w[i], c[i]) * inv;
+                    ss = __builtin_fmaf(v, v, ss);
+                }
+            }
+            ss = join_token<COLS, WN>(ss, AddF{}, red, stride, slot[tt], wn);
+            const bool zero = !live || (top < kTiny && as == as);
+            const float r = 1.0f / __builtin_sqrtf(ss);
+            if (in) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i] = zero ? 0.0f : scaled(get(tt, b, i), as, w[i], c[i]) * inv * r;
+                    store4(a.Y, a.out, t[tt], chan(b), a.N, vec, y);
+                }
+            }
+        } else {
+            // codes: y and its largest magnitude in float64, so that a value next
+            // to the middle between two codes is not moved across it
+            double top = 0.0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = __builtin_fmax(top, __builtin_fabs(scaled64(get(tt, b, i), (double)as, w[i], c[i])));
+            }
+            top = join_token<COLS, WN>(live ? top : 0.0, MaxF{}, red, stride, slot[tt], wn);
+            const bool zero = !(top >= (double)kTiny);
+            const double inv = zero ? 0.0 : 127.0 / top;
+            float ss = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
+                int q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const double v = scaled64(get(tt, b, i), (double)as, w[i], c[i]) * inv;
+                    q[i] = (int)__builtin_rint(v);
+                    ss = __builtin_fmaf((float)v, (float)v, ss);
+                }
+                if (in) store4_codes(a.Y, t[tt], chan(b), a.N, vec, q);
+            }
+            ss = join_token<COLS, WN>(ss, AddF{}, red, stride, slot[tt], wn);
+            if (in && wn == 0 && lane_id() < COLS) a.y_scale[t[tt]] = zero ? 1.0f : 1.0f / __builtin_sqrtf(ss);
+        }
+    });
+}
+
+// ---------------------------------------------------------------------------
+// Tiles through LDS
+// ---------------------------------------------------------------------------
+
+// position of 16-byte chunk c of a row of KB bytes, against bank conflicts
+template <int KB>
+__device__ __forceinline__ int place(int row, int c)
+{
+    if constexpr (KB == 128) return swz_chunk<128>(row, c);
+    else return c ^ ((row >> 2) & 3);  // 64-byte rows: four share a 256-byte bank line
+}
+
+template <int BT, int BN, int WT, int WN, int KB, int ST, bool EMBED, bool UNAL>
+struct Tile {
+    static constexpr int kWaves = WT * WN;
+    static constexpr int kThreads = kWaves * 64;
+    static constexpr int TT = BT / WT / 32;  // 32-token column tiles per wave
+    static constexpr int NT = BN / WN / 32;  // 32-channel row tiles per wave
+    static constexpr int kCpr = KB / 16;     // chunks per row
+    static constexpr int kLoads = (BT + BN) * kCpr / 64;              // wave-wide loads per stage
+    static constexpr int kPerWave = (kLoads + kWaves - 1) / kWaves;
+    static constexpr int kStage = (BT + BN) * KB;
+    static constexpr int kRows = 64 / kCpr;  // rows of one load
+    static_assert(BT % kRows == 0 && BN % kRows == 0, "a load stays inside one operand");
+    static_assert(ST == 2 || kLoads % kWaves == 0, "deep rings count their loads");
+};
+
+// One stage's MFMAs: the wave's channels x tokens, KB bytes of k from `buf`.
+template <typename C, int KB>
+__device__ __forceinline__ void multiply(const uint8_t* buf, int w_row, int a_row, i32x16 (&acc)[C::NT][C::TT])
+{
+    const int l = lane_id() & 31, h = lane_id() >> 5;
+#pragma unroll
+    for (int ks = 0; ks < KB / 32; ++ks) {
+        const int off = place<KB>(l, ks * 2 + h) * 16 + l * KB;
+        i32x4 w[C::NT], x[C::TT];
+#pragma unroll
+        for (int i = 0; i < C::NT; ++i) w[i] = *(const i32x4*)(buf + (w_row + i * 32) * KB + off);
+#pragma unroll
+        for (int i = 0; i < C::TT; ++i) x[i] = *(const i32x4*)(buf + (a_row + i * 32) * KB + off);
+#pragma unroll
+        for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+            for (int j = 0; j < C::TT; ++j) acc[i][j] = mfma32<kI8>(w[i], x[j], acc[i][j]);
+    }
+}
+
+template <int BT, int BN, int WT, int WN, int KB, int ST, bool EMBED, bool UNAL>
+__global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
+{
+    typedef Tile<BT, BN, WT, WN, KB, ST, EMBED, UNAL> C;
+    __shared__ __align__(1024) uint8_t ring[ST * C::kStage];
+    __shared__ __align__(16) float ws[BN], bs[BN];
+    __shared__ double red[EMBED && WN > 1 ? WN * BT : 1];
+
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
+    const int wt = wave / WN, wn = wave % WN;
+
+    // Workgroup to tile: consecutive workgroups go to the 8 XCDs in turn, so
+    // each XCD takes a contiguous run of tiles, walked in blocks of 8 token
+    // tiles, whose operands the XCD's L2 then holds.
+    int64_t t0;
+    int n0;
+    {
+        const int nwg = a.tiles_t * a.tiles_n, b = blockIdx.x;
+        const int q = nwg >> 3, r = nwg & 7, x = b & 7;
+        const int id = x * q + (x < r ? x : r) + (b >> 3);
+        const int per = 8 * a.tiles_n, band = id / per, in = id - band * per;
+        const int left = a.tiles_t - band * 8, high = left < 8 ? left : 8;
+        t0 = (int64_t)(band * 8 + in % high) * BT;
+        n0 = in / high * BN;
+    }
+    const int rows_t = (int)(a.T - t0 < BT ? a.T - t0 : BT);
+    const int rows_n = a.N - n0 < BN ? a.N - n0 : BN;
+    const int8_t* A = a.A + t0 * a.K;
+    const int8_t* W = a.W + (int64_t)n0 * a.K;
+    for (int i = threadIdx.x; i < BN; i += C::kThreads) {
+        ws[i] = i < rows_n ? a.w_scale[n0 + i] : 0.0f;
+        bs[i] = a.bias && i < rows_n ? a.bias[n0 + i] : 0.0f;
+    }
+
+    i32x16 acc[C::NT][C::TT];
+#pragma unroll
+    for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TT; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    const int a_row = wt * C::TT * 32, w_row = BT + wn * C::NT * 32;
+
+    // The wave's loads: load j covers kRows rows, one chunk per lane. Rows past
+    // the end of an operand repeat its last row; what they give is not stored.
+    uint32_t voff[C::kPerWave];
+    auto row_of = [&](int j) { return (wave * C::kPerWave + j) * C::kRows; };
+#pragma unroll
+    for (int j = 0; j < C::kPerWave; ++j) {
+        const int base = row_of(j), r = base + lane / C::kCpr;
+        const bool isA = base < BT;
+        const int local = isA ? r : r - BT, last = (isA ? rows_t : rows_n) - 1;
+        voff[j] = (uint32_t)(local < last ? local : last) * (uint32_t)a.K +
+                  (uint32_t)place<KB>(r, lane % C::kCpr) * 16;
+    }
+
+    const int nk = UNAL ? 0 : a.K / KB;  // stages filled by direct-to-LDS loads
+    if constexpr (!UNAL) {
+        const uint32_t ring0 = lds_addr(ring);
+        auto issue = [&](int i) {
+            const int8_t* pa = A + (int64_t)i * KB;
+            const int8_t* pw = W + (int64_t)i * KB;
+            const uint32_t at = ring0 + (uint32_t)(i % ST) * C::kStage;
+#pragma unroll
+            for (int j = 0; j < C::kPerWave; ++j) {
+                const int base = row_of(j);
+                if (C::kLoads % C::kWaves == 0 || base < BT + BN)
+                    dma_lds16(uniform_ptr(base < BT ? pa : pw), voff[j], uniform((int)(at + base * KB)));
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < ST - 1; ++s)
+            if (s < nk) issue(s);
+        for (int i = 0; i < nk; ++i) {
+            // stage i has landed: at most the loads of the ST - 2 later stages are out
+            if (ST > 2 && i + ST - 2 < nk) wait_vmcnt<(ST - 2) * C::kPerWave>();
+            else wait_vmcnt<0>();
+            block_barrier();  // all waves' loads of stage i landed; stage i - 1 is read
+            if (i + ST - 1 < nk) issue(i + ST - 1);
+            multiply<C, KB>(ring + (i % ST) * C::kStage, w_row, a_row, acc);
+        }
+    }
+    // The rest of k (all of it when rows are not 16-byte aligned) goes through
+    // registers, which fill up with zeros past the end of a row.
+    constexpr int kChunks = ((BT + BN) * C::kCpr + C::kThreads - 1) / C::kThreads;
+    for (int k0 = nk * KB; k0 < a.K; k0 += KB) {
+        i32x4 part[kChunks];
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int c = j * C::kThreads + threadIdx.x, r = c / C::kCpr;
+            const bool isA = r < BT;
+            const int local = isA ? r : r - BT, last = (isA ? rows_t : rows_n) - 1;
+            if (r < BT + BN)
+                part[j] = load16<UNAL>((isA ? A : W) + (int64_t)(local < last ? local : last) * a.K,
+                                       k0 + c % C::kCpr * 16, a.K);
+        }
+        __syncthreads();  // the stage's last readers are done
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int c = j * C::kThreads + threadIdx.x, r = c / C::kCpr;
+            if (r < BT + BN) *(i32x4*)(ring + r * KB + place<KB>(r, c % C::kCpr) * 16) = part[j];
+        }
+        __syncthreads();
+        multiply<C, KB>(ring, w_row, a_row, acc);
+    }
+    __syncthreads();  // ws and bs are written
+
+    const int half = lane >> 5;
+    if constexpr (EMBED) {
+        int64_t t[C::TT];
+        int slot[C::TT];
+#pragma unroll
+        for (int j = 0; j < C::TT; ++j) {
+            slot[j] = a_row + j * 32 + (lane & 31);
+            t[j] = t0 + slot[j];
+        }
+        embed_rows<C::TT, C::NT * 4, 32, WN>(
+            a, [&](int j, int b, int i) { return acc[b / 4][j][(b % 4) * 4 + i]; },
+            [&](int b) { return wn * C::NT * 32 + (b / 4) * 32 + (b % 4) * 8 + half * 4; }, ws, bs, t, slot, wn, red,
+            BT);
+    } else {
+        const bool vec = (a.N & 3) == 0;
+#pragma unroll
+        for (int j = 0; j < C::TT; ++j) {
+            const int64_t t = t0 + a_row + j * 32 + (lane & 31);
+            if (t >= a.T) continue;
+            const float as = a.a_scale[t];
+#pragma unroll
+            for (int i = 0; i < C::NT; ++i) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int n = wn * C::NT * 32 + i * 32 + b * 8 + half * 4;
+                    const f32x4 w = *(const f32x4*)(ws + n), c = *(const f32x4*)(bs + n);
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = scaled(acc[i][j][b * 4 + e], as, w[e], c[e]);
+                    store4(a.Y, a.out, t, n0 + n, a.N, vec, y);
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A few tokens
+// ---------------------------------------------------------------------------
+
+// TT tiles of 16 tokens x (NW * NPW) tiles of 16 channels per workgroup; NW
+// waves side by side over the channels, KW waves over k.
+template <int TT, int NPW, int NW, int KW, bool EMBED, bool UNAL>
+__global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
+{
+    constexpr int BN = NW * NPW * 16;
+    __shared__ __align__(16) float ws[BN], bs[BN];
+    __shared__ __align__(16) i32x4 sums[KW > 1 ? (KW - 1) * NW * NPW * TT * 64 : 1];
+    __shared__ double red[EMBED && NW > 1 ? NW * TT * 16 : 1];
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
+    const int kw = wave / NW, nw = wave % NW;
+    const int n0 = EMBED ? 0 : (int)blockIdx.x * BN;
+    const int64_t t0 = EMBED ? (int64_t)blockIdx.x * (TT * 16) : 0;
+    const int row = lane & 15, quarter = lane >> 4;
+
+    for (int i = threadIdx.x; i < BN; i += NW * KW * 64) {
+        ws[i] = n0 + i < a.N ? a.w_scale[n0 + i] : 0.0f;
+        bs[i] = a.bias && n0 + i < a.N ? a.bias[n0 + i] : 0.0f;
+    }
+    const int8_t* wp[NPW];
+    const int8_t* ap[TT];
+#pragma unroll
+    for (int p = 0; p < NPW; ++p) {
+        const int n = n0 + (nw * NPW + p) * 16 + row;
+        wp[p] = a.W + (int64_t)(n < a.N ? n : a.N - 1) * a.K;
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int64_t t = t0 + j * 16 + row;
+        ap[j] = a.A + (t < a.T ? t : a.T - 1) * a.K;
+    }
+    i32x4 acc[NPW][TT];
+#pragma unroll
+    for (int p = 0; p < NPW; ++p)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[p][j] = i32x4{};
+
+    const int steps = (a.K + 63) / 64, per = (steps + KW - 1) / KW;
+    const int s1 = (kw + 1) * per < steps ? (kw + 1) * per : steps;
+    constexpr int U = TT + NPW <= 2 ? 8 : TT + NPW <= 4 ? 4 : 2;  // steps whose loads fly together
+    for (int s = kw * per; s < s1; s += U) {
+        i32x4 w[U][NPW], x[U][TT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = s + u < s1 ? (s + u) * 64 + quarter * 16 : a.K;  // k >= K gives zeros
+#pragma unroll
+            for (int p = 0; p < NPW; ++p) w[u][p] = load16<UNAL>(wp[p], k, a.K);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) x[u][j] = load16<UNAL>(ap[j], k, a.K);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int p = 0; p < NPW; ++p)
+#pragma unroll
+                for (int j = 0; j < TT; ++j)
+                    acc[p][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][p], x[u][j], acc[p][j], 0, 0, 0);
+    }
+    if constexpr (KW > 1) {
+        if (kw > 0) {
+#pragma unroll
+            for (int p = 0; p < NPW; ++p)
+#pragma unroll
+                for (int j = 0; j < TT; ++j) sums[((((kw - 1) * NW + nw) * NPW + p) * TT + j) * 64 + lane] = acc[p][j];
+        }
+    }
+    __syncthreads();
+    if constexpr (KW > 1) {
+        if (kw == 0) {
+            for (int o = 0; o < KW - 1; ++o) {
+#pragma unroll
+                for (int p = 0; p < NPW; ++p)
+#pragma unroll
+                    for (int j = 0; j < TT; ++j) acc[p][j] += sums[(((o * NW + nw) * NPW + p) * TT + j) * 64 + lane];
+            }
+        }
+    }
+    if constexpr (EMBED) {
+        // the waves of other k parts only keep the barriers: they hold no rows
+        int64_t t[TT];
+        int slot[TT];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            slot[j] = j * 16 + row;
+            t[j] = kw == 0 ? t0 + slot[j] : a.T;
+        }
+        embed_rows<TT, NPW, 16, NW>(
+            a, [&](int j, int b, int i) { return acc[b][j][i]; },
+            [&](int b) { return (nw * NPW + b) * 16 + quarter * 4; }, ws, bs, t, slot, kw == 0 ? nw : -1, red, TT * 16);
+    } else {
+        if (kw > 0) return;
+        const bool vec = (a.N & 3) == 0;
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const int64_t t = t0 + j * 16 + row;
+            if (t >= a.T) continue;
+            const float as = a.a_scale[t];
+#pragma unroll
+            for (int p = 0; p < NPW; ++p) {
+                const int n = (nw * NPW + p) * 16 + quarter * 4;
+                const f32x4 w = *(const f32x4*)(ws + n), c = *(const f32x4*)(bs + n);
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = scaled(acc[p][j][e], as, w[e], c[e]);
+                store4(a.Y, a.out, t, n0 + n, a.N, vec, y);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+
+int64_t tiles(int64_t n, int b) { return (n + b - 1) / b; }
+
+template <int BT, int BN, int WT, int WN, int KB, int ST, bool EMBED, bool UNAL>
+void run_tiles(LinearArgs a, hipStream_t stream)
+{
+    a.tiles_t = (int32_t)tiles(a.T, BT);
+    a.tiles_n = (int32_t)tiles(a.N, BN);
+    hipLaunchKernelGGL((tile_kernel<BT, BN, WT, WN, KB, ST, EMBED, UNAL>), dim3((unsigned)(a.tiles_t * a.tiles_n)),
+                       dim3(WT * WN * 64), 0, stream, a);
+}
+
+template <int TT, int NPW, int NW, int KW, bool EMBED>
+void run_few(const LinearArgs& a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(EMBED ? tiles(a.T, TT * 16) : tiles(a.N, NW * NPW * 16))), block(NW * KW * 64);
+    if (a.K % 16 == 0) hipLaunchKernelGGL((few_kernel<TT, NPW, NW, KW, EMBED, false>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((few_kernel<TT, NPW, NW, KW, EMBED, true>), grid, block, 0, stream, a);
+}
+
+void linear_once(const LinearArgs& a, hipStream_t stream)
+{
+    const int cus = device_cu_count();
+    const bool unal = a.K % 16 != 0;
+    if (a.T <= 16) run_few<1, 1, 1, 8, false>(a, stream);
+    else if (a.T <= 32) run_few<2, 1, 1, 8, false>(a, stream);
+    else if (a.T <= 64) run_few<4, 1, 1, 8, false>(a, stream);
+    else if (unal) run_tiles<128, 128, 2, 2, 128, 2, false, true>(a, stream);
+    else if (tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 128, 2, false, false>(a, stream);
+    else if (tiles(a.T, 128) * tiles(a.N, 128) >= cus) run_tiles<128, 128, 2, 2, 128, 2, false, false>(a, stream);
+    else run_tiles<64, 64, 2, 2, 128, 4, false, false>(a, stream);
+}
+
+template <bool UNAL>
+void embed_tiles(const LinearArgs& a, hipStream_t stream)
+{
+    if (a.N <= 128) run_tiles<256, 128, 8, 1, 128, 2, true, UNAL>(a, stream);
+    else if (a.N <= 256) run_tiles<128, 256, 4, 2, 128, 2, true, UNAL>(a, stream);
+    else if (a.N <= 512) run_tiles<64, 512, 2, 4, 128, 2, true, UNAL>(a, stream);
+    else run_tiles<64, 1024, 1, 8, 64, 2, true, UNAL>(a, stream);
+}
+
+void embed_once(const LinearArgs& a, hipStream_t stream)
+{
+    if (a.T <= 4096) {
+        if (a.N <= 128) run_few<1, 1, 8, 2, true>(a, stream);
+        else if (a.N <= 256) run_few<1, 1, 16, 1, true>(a, stream);
+        else if (a.N <= 512) run_few<1, 2, 16, 1, true>(a, stream);
+        else run_few<1, 4, 16, 1, true>(a, stream);
+    } else if (a.K % 16 == 0) {
+        embed_tiles<false>(a, stream);
+    } else {
+        embed_tiles<true>(a, stream);
+    }
+}
+
+// One launch covers at most `step` rows, so that a grid's threads stay below
+// 2^32; the rows are independent.
+template <typename F>
+hipError_t by_rows(LinearArgs a, int64_t step, F once)
+{
+    const int64_t es = a.out == kF32 ? 4 : a.out == kI8 ? 1 : 2;
+    for (int64_t left = a.T; left > 0; left -= step) {
+        a.T = left < step ? left : step;
+        once(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.A += step * a.K;
+        a.a_scale += step;
+        if (a.mask) a.mask += step;
+        a.Y = (char*)a.Y + step * a.N * es;
+        if (a.y_scale) a.y_scale += step;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_linear_i8(LinearArgs a, hipStream_t stream)
+{
+    // N is at most 2^26, so 256 rows make at most 2^22 tiles of 64 x 64
+    int64_t step = (int64_t)1 << 24;
+    while (step > 256 && tiles(step, 64) * tiles(a.N, 64) > (1 << 22)) step /= 2;
+    return by_rows(a, step, [&](const LinearArgs& x) { linear_once(x, stream); });
+}
+
+hipError_t launch_embed_i8(LinearArgs a, hipStream_t stream)
+{
+    return by_rows(a, (int64_t)1 << 26, [&](const LinearArgs& x) { embed_once(x, stream); });
+}
+
+}  // namespace maxsim

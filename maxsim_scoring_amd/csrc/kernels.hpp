@@ -135,6 +135,49 @@ struct TopkArgs {
     int32_t* rows;       // [Nq, K] row index of each entry, or null
 };
 
+// Rows of the embedding head (quantisation, normalisation and its gradient).
+// Element codes are Elem's kF16, kBF16 and kF32.
+struct RowArgs {
+    const void* X;        // [T, d]
+    const uint8_t* mask;  // [T] or null
+    const float* rnorm;   // [T] (gradient)
+    const float* g;       // [T, d] upstream gradient
+    void* Y;              // [T, d] codes, unit rows or gradient
+    float* stat;          // [T] scale or rnorm (outputs)
+    int64_t T;
+    int32_t d;
+    int out;        // element type of Y (float outputs)
+    int normalize;  // quantisation: scale codes to unit rows
+};
+
+struct DropArgs {
+    const void* X;
+    void* Y;
+    int64_t n;
+    uint32_t seed_lo, seed_hi;
+    uint64_t step;
+    const uint64_t* step_dev;  // added to step, or null
+    uint32_t q;                // drop where 16 random bits are below q
+    float up;                  // 65536 / (65536 - q), 0 for q = 65536
+};
+
+// 8-bit product with token and channel scales, rows optionally normalised.
+struct LinearArgs {
+    const int8_t* A;       // [T, K]
+    const float* a_scale;  // [T]
+    const int8_t* W;       // [N, K]
+    const float* w_scale;  // [N]
+    const float* bias;     // [N] or null
+    const uint8_t* mask;   // [T] or null (embeddings)
+    void* Y;               // [T, N]
+    float* y_scale;        // [T] (codes)
+    int64_t T;
+    int32_t N, K;
+    int out;  // element type of Y (kI8: codes)
+    // filled by the launcher
+    int32_t tiles_t, tiles_n;
+};
+
 constexpr int kTopkMaxK = 1024;  // largest k of one top-k call
 
 // Compute units of the current device (queried once per device, thread-safe).
@@ -148,5 +191,11 @@ hipError_t launch_topk(TopkArgs a, hipStream_t stream);
 hipError_t launch_bwd_varlen(int elem, VarBwdArgs a, hipStream_t stream);
 hipError_t launch_chamfer_fwd(ChamferArgs a, hipStream_t stream);
 hipError_t launch_chamfer_bwd(ChamferArgs a, hipStream_t stream);
+hipError_t launch_quantize(int elem, RowArgs a, hipStream_t stream);
+hipError_t launch_normalize_fwd(int elem, RowArgs a, hipStream_t stream);
+hipError_t launch_normalize_bwd(int elem, RowArgs a, hipStream_t stream);
+hipError_t launch_dropout(int elem, DropArgs a, hipStream_t stream);
+hipError_t launch_linear_i8(LinearArgs a, hipStream_t stream);
+hipError_t launch_embed_i8(LinearArgs a, hipStream_t stream);
 
 }  // namespace maxsim
