@@ -26,6 +26,7 @@ namespace {
 constexpr float kTiny = 0x1p-110f;  // rows below this count as zeros
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
 
 __device__ __forceinline__ uint32_t half_bits(int out, float v)
@@ -67,38 +68,70 @@ __device__ __forceinline__ double scaled64(int acc, double as, float ws, float b
     return (double)acc * (as * (double)ws) + (double)b;
 }
 
-// Four consecutive outputs n .. n + 3 of row t. vec: N is a multiple of 4.
-__device__ __forceinline__ void store4(void* Y, int out, int64_t t, int n, int N, bool vec, const float (&y)[4])
+// R (4 or 16) consecutive outputs n .. n + R - 1 of row t, those below N, in
+// pieces of up to 16 bytes where N keeps every row aligned for them.
+template <int R>
+__device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, int N, const float (&y)[R])
 {
     const int64_t at = t * N + n;
-    if (vec) {
-        if (n >= N) return;
-        if (out == kF32) {
-            *(f32x4*)((float*)Y + at) = f32x4{y[0], y[1], y[2], y[3]};
+    if (out == kF32) {
+        float* p = (float*)Y + at;
+        if ((N & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i)
+                if (n + 4 * i < N) ((f32x4*)p)[i] = f32x4{y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
         } else {
-            *(u32x2*)((uint16_t*)Y + at) = u32x2{half_bits(out, y[0]) | half_bits(out, y[1]) << 16,
-                                                half_bits(out, y[2]) | half_bits(out, y[3]) << 16};
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (n + i < N) p[i] = y[i];
+        }
+        return;
+    }
+    uint16_t* p = (uint16_t*)Y + at;
+    uint32_t w[R / 2];
+    if (out == kBF16) {
+#pragma unroll
+        for (int i = 0; i < R / 2; ++i) w[i] = half_bits(kBF16, y[2 * i]) | half_bits(kBF16, y[2 * i + 1]) << 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < R / 2; ++i) w[i] = half_bits(kF16, y[2 * i]) | half_bits(kF16, y[2 * i + 1]) << 16;
+    }
+    if (R == 16 && (N & 7) == 0) {
+#pragma unroll
+        for (int i = 0; i < R / 8; ++i)
+            if (n + 8 * i < N) ((u32x4*)p)[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    } else if ((N & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < R / 4; ++i)
+            if (n + 4 * i < N) ((u32x2*)p)[i] = u32x2{w[2 * i], w[2 * i + 1]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (n + i < N) p[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+    }
+}
+// The same for codes, each in the low byte of a word.
+template <int R>
+__device__ __forceinline__ void store_codes(void* Y, int64_t t, int n, int N, const uint32_t (&q)[R])
+{
+    int8_t* p = (int8_t*)Y + t * N + n;
+    if ((N & 3) == 0) {
+        uint32_t w[R / 4];
+#pragma unroll
+        for (int i = 0; i < R / 4; ++i)
+            w[i] = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0c0c0400u) |
+                   __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x0c0c0400u) << 16;
+        if (R == 16 && (N & 15) == 0) {
+            if (n < N) *(u32x4*)p = u32x4{w[0], w[R / 4 > 1 ? 1 : 0], w[R / 4 > 2 ? 2 : 0], w[R / 4 > 3 ? 3 : 0]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i)
+                if (n + 4 * i < N) ((uint32_t*)p)[i] = w[i];
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= N) return;
-        if (out == kF32) ((float*)Y)[at + i] = y[i];
-        else ((uint16_t*)Y)[at + i] = (uint16_t)half_bits(out, y[i]);
-    }
-}
-__device__ __forceinline__ void store4_codes(void* Y, int64_t t, int n, int N, bool vec, const int (&q)[4])
-{
-    int8_t* p = (int8_t*)Y + t * N + n;
-    if (vec) {
-        if (n < N)
-            *(uint32_t*)p = (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 |
-                            (uint32_t)q[3] << 24;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
         if (n + i < N) p[i] = (int8_t)q[i];
 }
 
@@ -112,113 +145,125 @@ __device__ __forceinline__ void static_for(F&& f)
     }
 }
 
-struct AddF { template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a + b; } };
-struct MaxF {
-    __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_fmaxf(a, b); }
-    __device__ __forceinline__ double operator()(double a, double b) const { return __builtin_fmax(a, b); }
-};
-
-__device__ __forceinline__ float xor_lane(float v, int m) { return shfl_xor_f(v, m); }
 __device__ __forceinline__ double xor_lane(double v, int m) { return __shfl_xor(v, m, 64); }
 
-// Joins one value per token over the lanes that share it (lane / COLS) and over
-// the WN waves that hold other channels, in a fixed order. `red` holds WN rows
-// of `stride` doubles; `slot` is the token's place in a row. Every wave of the
-// workgroup calls it; those that hold no sums pass wn < 0.
-template <int COLS, int WN, typename V, typename OP>
-__device__ __forceinline__ V join_token(V v, OP op, double* red, int stride, int slot, int wn)
+// The largest magnitude and the sum of squares of the rows that a workgroup
+// holds: joins each token's pair over the lanes that share it (lane / COLS) and
+// over the WN waves that hold other channels, in a fixed order. red holds
+// 2 x WN rows of `stride`; slot is the token's place in a row. Every wave of the
+// workgroup calls it once between two other barriers; waves that hold no sums
+// pass wn < 0.
+template <int TT, int COLS, int WN>
+__device__ __forceinline__ void join_rows(double (&top)[TT], double (&ss)[TT], double* red, int stride,
+                                          const int (&slot)[TT], int wn)
 {
 #pragma unroll
-    for (int m = COLS; m < 64; m *= 2) v = op(v, xor_lane(v, m));
-    if constexpr (WN > 1) {
-        __syncthreads();
-        if (wn >= 0 && lane_id() < COLS) red[wn * stride + slot] = (double)v;
-        __syncthreads();
-        v = (V)red[slot];
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int w = 1; w < WN; ++w) v = op(v, (V)red[w * stride + slot]);
+        for (int m = COLS; m < 64; m *= 2) {
+            top[t] = __builtin_fmax(top[t], xor_lane(top[t], m));
+            ss[t] += xor_lane(ss[t], m);
+        }
+    if constexpr (WN > 1) {
+        if (wn >= 0 && lane_id() < COLS) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                red[wn * stride + slot[t]] = top[t];
+                red[(WN + wn) * stride + slot[t]] = ss[t];
+            }
+        }
+        block_barrier();
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            top[t] = red[slot[t]];
+            ss[t] = red[WN * stride + slot[t]];
+#pragma unroll
+            for (int w = 1; w < WN; ++w) {
+                top[t] = __builtin_fmax(top[t], red[w * stride + slot[t]]);
+                ss[t] += red[(WN + w) * stride + slot[t]];
+            }
+        }
     }
-    return v;
 }
 
-// Normalises the rows that a workgroup holds and writes them. A lane holds, for
-// each of TT tokens, NB groups of 4 consecutive channels: get(tt, b, i) is the
-// int32 sum, chan(b) the first channel of group b. ws and bs (LDS) hold the
-// scales and biases of the workgroup's channels, 0 past the last one.
-template <int TT, int NB, int COLS, int WN, typename GET, typename CHAN>
+// Normalises the rows that a workgroup holds and writes them. For each of TT
+// tokens a lane holds NB runs of R consecutive channels: get(tt, b, i) is the
+// int32 sum of channel chan(b) + i. ws and bs (LDS) hold the scales and biases
+// of the workgroup's channels, 0 past the last one.
+//
+// With s the largest magnitude of the row, its values over the norm are
+// (y / s) * (s / ||y||), whose factors neither overflow nor vanish; the sum of
+// squares is a float64, which holds the square of every float32 y. Codes are
+// the nearest integers to 127 y / s: y and s are float64 there, so that a value
+// next to the middle between two codes is not moved across it, and adding
+// 1.5 * 2^52 in the product's fma leaves the integer in the low bits.
+template <int TT, int NB, int R, int COLS, int WN, typename GET, typename CHAN>
 __device__ __forceinline__ void embed_rows(const LinearArgs& a, GET get, CHAN chan, const float* ws, const float* bs,
-                                           const int64_t (&t)[TT], const int (&slot)[TT], int wn, double* red,
-                                           int stride)
+                                           const int64_t (&t)[TT], const float (&as)[TT], const bool (&live)[TT],
+                                           const int (&slot)[TT], int wn, double* red, int stride)
 {
-    const bool vec = (a.N & 3) == 0;
+    double top[TT], ss[TT];
+    static_for<0, TT>([&](auto tt) {
+        double s2 = 0.0;
+        if (a.out != kI8) {
+            float m = 0.0f;
+            static_for<0, NB>([&](auto b) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float y = scaled(get(tt, b, i), as[tt], ws[chan(b) + i], bs[chan(b) + i]);
+                    m = __builtin_fmaxf(m, __builtin_fabsf(y));
+                    s2 = __builtin_fma((double)y, (double)y, s2);
+                }
+            });
+            top[tt] = live[tt] ? (double)m : 0.0;
+        } else {
+            double m = 0.0;
+            static_for<0, NB>([&](auto b) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const double y = scaled64(get(tt, b, i), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
+                    m = __builtin_fmax(m, __builtin_fabs(y));
+                    s2 = __builtin_fma(y, y, s2);
+                }
+            });
+            top[tt] = live[tt] ? m : 0.0;
+        }
+        ss[tt] = s2;
+    });
+    join_rows<TT, COLS, WN>(top, ss, red, stride, slot, wn);
     static_for<0, TT>([&](auto tt) {
         const bool in = t[tt] < a.T;
-        const bool live = in && (!a.mask || a.mask[t[tt]]);
-        const float as = live ? a.a_scale[t[tt]] : 0.0f;
         if (a.out != kI8) {
-            float top = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = __builtin_fmaxf(top, __builtin_fabsf(scaled(get(tt, b, i), as, w[i], c[i])));
-            }
-            top = join_token<COLS, WN>(live ? top : 0.0f, MaxF{}, red, stride, slot[tt], wn);
-            const float inv = 1.0f / top;
-            float ss = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float v = scaled(get(tt, b, i), as, w[i], c[i]) * inv;
-                    ss = __builtin_fmaf(v, v, ss);
-                }
-            }
-            ss = join_token<COLS, WN>(ss, AddF{}, red, stride, slot[tt], wn);
-            const bool zero = !live || (top < kTiny && as == as);
-            const float r = 1.0f / __builtin_sqrtf(ss);
+            const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
+            const float inv = 1.0f / (float)top[tt];
+            const float r = (float)(top[tt] / __builtin_sqrt(ss[tt]));
             if (in) {
+                static_for<0, NB>([&](auto b) {
+                    float y[R];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
-                    float y[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        y[i] = zero ? 0.0f : scaled(get(tt, b, i), as, w[i], c[i]) * inv * r;
-                    store4(a.Y, a.out, t[tt], chan(b), a.N, vec, y);
-                }
+                    for (int i = 0; i < R; ++i)
+                        y[i] = zero ? 0.0f
+                                    : scaled(get(tt, b, i), as[tt], ws[chan(b) + i], bs[chan(b) + i]) * inv * r;
+                    store_run<R>(a.Y, a.out, t[tt], chan(b), a.N, y);
+                });
             }
         } else {
-            // codes: y and its largest magnitude in float64, so that a value next
-            // to the middle between two codes is not moved across it
-            double top = 0.0;
+            const bool zero = !(top[tt] >= (double)kTiny);
+            const double inv = zero ? 0.0 : 127.0 / top[tt];
+            if (in) {
+                static_for<0, NB>([&](auto b) {
+                    uint32_t q[R];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = __builtin_fmax(top, __builtin_fabs(scaled64(get(tt, b, i), (double)as, w[i], c[i])));
+                    for (int i = 0; i < R; ++i) {
+                        const double y = scaled64(get(tt, b, i), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
+                        q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(zero ? 0.0 : y, inv, 0x1.8p52));
+                    }
+                    store_codes<R>(a.Y, t[tt], chan(b), a.N, q);
+                });
+                // codes * scale is y / ||y||, so scale = s / (127 ||y||)
+                if (wn == 0 && lane_id() < COLS)
+                    a.y_scale[t[tt]] = zero ? 1.0f : (float)(top[tt] / (127.0 * __builtin_sqrt(ss[tt])));
             }
-            top = join_token<COLS, WN>(live ? top : 0.0, MaxF{}, red, stride, slot[tt], wn);
-            const bool zero = !(top >= (double)kTiny);
-            const double inv = zero ? 0.0 : 127.0 / top;
-            float ss = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const f32x4 w = *(const f32x4*)(ws + chan(b)), c = *(const f32x4*)(bs + chan(b));
-                int q[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const double v = scaled64(get(tt, b, i), (double)as, w[i], c[i]) * inv;
-                    q[i] = (int)__builtin_rint(v);
-                    ss = __builtin_fmaf((float)v, (float)v, ss);
-                }
-                if (in) store4_codes(a.Y, t[tt], chan(b), a.N, vec, q);
-            }
-            ss = join_token<COLS, WN>(ss, AddF{}, red, stride, slot[tt], wn);
-            if (in && wn == 0 && lane_id() < COLS) a.y_scale[t[tt]] = zero ? 1.0f : 1.0f / __builtin_sqrtf(ss);
         }
     });
 }
@@ -233,6 +278,14 @@ __device__ __forceinline__ int place(int row, int c)
 {
     if constexpr (KB == 128) return swz_chunk<128>(row, c);
     else return c ^ ((row >> 2) & 3);  // 64-byte rows: four share a 256-byte bank line
+}
+
+// Which channel of its 32 an MFMA row stands for. A lane's 16 results are rows
+// 8 b + 4 h + e of its half h; with this order they are 16 consecutive channels,
+// 16 h + 4 b + e, and are stored as one run.
+__device__ __forceinline__ int channel_of(int row)
+{
+    return (row & ~31) | (row & 4) << 2 | (row & 24) >> 1 | (row & 3);
 }
 
 template <int BT, int BN, int WT, int WN, int KB, int ST, bool EMBED, bool UNAL>
@@ -276,7 +329,7 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
     typedef Tile<BT, BN, WT, WN, KB, ST, EMBED, UNAL> C;
     __shared__ __align__(1024) uint8_t ring[ST * C::kStage];
     __shared__ __align__(16) float ws[BN], bs[BN];
-    __shared__ double red[EMBED && WN > 1 ? WN * BT : 1];
+    __shared__ double red[EMBED && WN > 1 ? 2 * WN * BT : 1];
 
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int wt = wave / WN, wn = wave % WN;
@@ -321,7 +374,7 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
     for (int j = 0; j < C::kPerWave; ++j) {
         const int base = row_of(j), r = base + lane / C::kCpr;
         const bool isA = base < BT;
-        const int local = isA ? r : r - BT, last = (isA ? rows_t : rows_n) - 1;
+        const int local = isA ? r : channel_of(r - BT), last = (isA ? rows_t : rows_n) - 1;
         voff[j] = (uint32_t)(local < last ? local : last) * (uint32_t)a.K +
                   (uint32_t)place<KB>(r, lane % C::kCpr) * 16;
     }
@@ -336,8 +389,11 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
 #pragma unroll
             for (int j = 0; j < C::kPerWave; ++j) {
                 const int base = row_of(j);
-                if (C::kLoads % C::kWaves == 0 || base < BT + BN)
-                    dma_lds16(uniform_ptr(base < BT ? pa : pw), voff[j], uniform((int)(at + base * KB)));
+                const uint32_t to = (uint32_t)uniform((int)(at + base * KB));
+                // embeddings: the hidden states pass once, W is read by every workgroup
+                if (EMBED && base < BT) dma_lds16_nt(uniform_ptr(pa), voff[j], to);
+                else if (C::kLoads % C::kWaves == 0 || base < BT + BN)
+                    dma_lds16(uniform_ptr(base < BT ? pa : pw), voff[j], to);
             }
         };
 #pragma unroll
@@ -361,7 +417,7 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
         for (int j = 0; j < kChunks; ++j) {
             const int c = j * C::kThreads + threadIdx.x, r = c / C::kCpr;
             const bool isA = r < BT;
-            const int local = isA ? r : r - BT, last = (isA ? rows_t : rows_n) - 1;
+            const int local = isA ? r : channel_of(r - BT), last = (isA ? rows_t : rows_n) - 1;
             if (r < BT + BN)
                 part[j] = load16<UNAL>((isA ? A : W) + (int64_t)(local < last ? local : last) * a.K,
                                        k0 + c % C::kCpr * 16, a.K);
@@ -381,17 +437,19 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
     if constexpr (EMBED) {
         int64_t t[C::TT];
         int slot[C::TT];
+        float as[C::TT];
+        bool live[C::TT];
 #pragma unroll
         for (int j = 0; j < C::TT; ++j) {
             slot[j] = a_row + j * 32 + (lane & 31);
             t[j] = t0 + slot[j];
+            live[j] = t[j] < a.T && (!a.mask || a.mask[t[j]]);
+            as[j] = live[j] ? a.a_scale[t[j]] : 0.0f;
         }
-        embed_rows<C::TT, C::NT * 4, 32, WN>(
-            a, [&](int j, int b, int i) { return acc[b / 4][j][(b % 4) * 4 + i]; },
-            [&](int b) { return wn * C::NT * 32 + (b / 4) * 32 + (b % 4) * 8 + half * 4; }, ws, bs, t, slot, wn, red,
-            BT);
+        embed_rows<C::TT, C::NT, 16, 32, WN>(
+            a, [&](auto j, auto b, int i) { return acc[b][j][i]; },
+            [&](int b) { return (wn * C::NT + b) * 32 + half * 16; }, ws, bs, t, as, live, slot, wn, red, BT);
     } else {
-        const bool vec = (a.N & 3) == 0;
 #pragma unroll
         for (int j = 0; j < C::TT; ++j) {
             const int64_t t = t0 + a_row + j * 32 + (lane & 31);
@@ -399,17 +457,115 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
             const float as = a.a_scale[t];
 #pragma unroll
             for (int i = 0; i < C::NT; ++i) {
+                const int n = (wn * C::NT + i) * 32 + half * 16;
+                float y[16];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int n = wn * C::NT * 32 + i * 32 + b * 8 + half * 4;
-                    const f32x4 w = *(const f32x4*)(ws + n), c = *(const f32x4*)(bs + n);
-                    float y[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = scaled(acc[i][j][b * 4 + e], as, w[e], c[e]);
-                    store4(a.Y, a.out, t, n0 + n, a.N, vec, y);
-                }
+                for (int e = 0; e < 16; ++e) y[e] = scaled(acc[i][j][e], as, ws[n + e], bs[n + e]);
+                store_run<16>(a.Y, a.out, t, n0 + n, a.N, y);
             }
         }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens through a narrow projection
+// ---------------------------------------------------------------------------
+
+// For embeddings of up to NWV x 32 channels of K <= KS x 32 (a multiple of 128)
+// the weights fit in registers: each of NWV waves keeps its 32 channels for the
+// whole run, and the hidden states stream through an LDS ring of ST stages, 32
+// whole rows each, one contiguous piece of memory. Nothing but the states is
+// read again and again, each byte once.
+template <int KS, int NWV, int ST>
+__global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
+{
+    constexpr int kScales = KS * 1024, kMask = kScales + 256, kStage = kMask + 256;
+    constexpr int PW = (KS + NWV - 1) / NWV;  // wave-wide loads of rows per wave and stage
+    constexpr int kLoads = PW + 2;            // and the tokens' scales and mask
+    __shared__ __align__(1024) uint8_t ring[ST * kStage];
+    __shared__ __align__(16) float ws[NWV * 32], bs[NWV * 32];
+    __shared__ double red[2 * NWV * 32];
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id(), l = lane & 31, half = lane >> 5;
+    const int K = a.K;
+
+    for (int i = threadIdx.x; i < NWV * 32; i += NWV * 64) {
+        ws[i] = i < a.N ? a.w_scale[i] : 0.0f;
+        bs[i] = a.bias && i < a.N ? a.bias[i] : 0.0f;
+    }
+    i32x4 w[KS];
+    {
+        const int n = wave * 32 + channel_of(l);
+        const int8_t* row = a.W + (int64_t)(n < a.N ? n : 0) * K;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) w[s] = load16<false>(row, n < a.N ? s * 32 + half * 16 : K, K);
+    }
+
+    // 16-byte chunk c of row r lies at chunk c ^ f(r) of its row, so that 16
+    // lanes that read one chunk of consecutive rows meet no bank twice: rows are
+    // a multiple of 256 bytes apart, or an odd multiple of 128
+    const bool even = (K & 255) == 0;
+    auto f = [&](int r) { return even ? r & 15 : (r >> 1) & 7; };
+    const int cpr = K / 16, loads = K / 32;
+    int row_of[PW], at_of[PW];
+#pragma unroll
+    for (int j = 0; j < PW; ++j) {
+        const int load = wave * PW + j < loads ? wave * PW + j : loads - 1;  // a spare load repeats the last
+        const int p = load * 64 + lane;
+        row_of[j] = p / cpr;
+        at_of[j] = ((p % cpr) ^ f(row_of[j])) * 16;
+    }
+    const uint32_t ring0 = lds_addr(ring);
+    const int count = (a.tiles_t - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;  // tiles of this workgroup
+    auto issue = [&](int i) {
+        const int64_t t0 = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * 32;
+        const int last = (int)(a.T - t0 < 32 ? a.T - t0 : 32) - 1;
+        const uint32_t to = ring0 + (uint32_t)(i % ST) * kStage;
+        const void* src = uniform_ptr(a.A + t0 * K);
+#pragma unroll
+        for (int j = 0; j < PW; ++j) {
+            const int load = wave * PW + j < loads ? wave * PW + j : loads - 1;
+            dma_lds16_nt(src, (uint32_t)((row_of[j] < last ? row_of[j] : last) * K + at_of[j]),
+                         (uint32_t)uniform((int)(to + load * 1024)));
+        }
+        // every wave brings the 32 scales and mask bytes, so that all count alike
+        dma_lds4(uniform_ptr(a.a_scale + t0), (uint32_t)(lane < last ? lane : last) * 4,
+                 (uint32_t)uniform((int)(to + kScales)));
+        // the aligned words that hold the tile's mask bytes, and only those
+        const uintptr_t m = a.mask ? (uintptr_t)(a.mask + t0) : (uintptr_t)(a.a_scale + t0);
+        const int words = ((int)(m & 3) + last + 4) >> 2;
+        dma_lds4(uniform_ptr((const void*)(m & ~(uintptr_t)3)), (uint32_t)(lane < words ? lane : words - 1) * 4,
+                 (uint32_t)uniform((int)(to + kMask)));
+    };
+    const int mask_at = a.mask ? (int)((uintptr_t)a.mask & 3) : 0;  // tiles start at multiples of 32
+    int off[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) off[j] = l * K + ((2 * j + half) ^ f(l)) * 16;
+
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s)
+        if (s < count) issue(s);
+    for (int i = 0; i < count; ++i) {
+        if (i + ST - 2 < count) wait_vmcnt<(ST - 2) * kLoads>();
+        else wait_vmcnt<0>();
+        block_barrier();  // all waves' loads of stage i landed; stage i - 1 is read
+        if (i + ST - 1 < count) issue(i + ST - 1);
+        const uint8_t* st = ring + (i % ST) * kStage;
+        i32x16 acc;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[r] = 0;
+        // where K < KS * 32, the last fragments of w are zeros and the bytes they
+        // meet are those of other rows
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            acc = mfma32<kI8>(w[s], *(const i32x4*)(st + off[s & 7] + (s >> 3) * 256), acc);
+        const int64_t t0 = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * 32;
+        const int64_t t[1] = {t0 + l};
+        const bool live[1] = {t[0] < a.T && (!a.mask || st[kMask + mask_at + l])};
+        const float as[1] = {live[0] ? *(const float*)(st + kScales + l * 4) : 0.0f};
+        const int slot[1] = {l};
+        embed_rows<1, 1, 16, 32, NWV>(
+            a, [&](auto, auto, int r) { return acc[r]; }, [&](int) { return wave * 32 + half * 16; }, ws, bs, t, as,
+            live, slot, wave, red, 32);
     }
 }
 
@@ -425,7 +581,7 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
     constexpr int BN = NW * NPW * 16;
     __shared__ __align__(16) float ws[BN], bs[BN];
     __shared__ __align__(16) i32x4 sums[KW > 1 ? (KW - 1) * NW * NPW * TT * 64 : 1];
-    __shared__ double red[EMBED && NW > 1 ? NW * TT * 16 : 1];
+    __shared__ double red[EMBED && NW > 1 ? 2 * NW * TT * 16 : 1];
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int kw = wave / NW, nw = wave % NW;
     const int n0 = EMBED ? 0 : (int)blockIdx.x * BN;
@@ -498,17 +654,21 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
         // the waves of other k parts only keep the barriers: they hold no rows
         int64_t t[TT];
         int slot[TT];
+        float as[TT];
+        bool live[TT];
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
             slot[j] = j * 16 + row;
             t[j] = kw == 0 ? t0 + slot[j] : a.T;
+            live[j] = t[j] < a.T && (!a.mask || a.mask[t[j]]);
+            as[j] = live[j] ? a.a_scale[t[j]] : 0.0f;
         }
-        embed_rows<TT, NPW, 16, NW>(
-            a, [&](int j, int b, int i) { return acc[b][j][i]; },
-            [&](int b) { return (nw * NPW + b) * 16 + quarter * 4; }, ws, bs, t, slot, kw == 0 ? nw : -1, red, TT * 16);
+        embed_rows<TT, NPW, 4, 16, NW>(
+            a, [&](auto j, auto b, int i) { return acc[b][j][i]; },
+            [&](int b) { return (nw * NPW + b) * 16 + quarter * 4; }, ws, bs, t, as, live, slot, kw == 0 ? nw : -1, red,
+            TT * 16);
     } else {
         if (kw > 0) return;
-        const bool vec = (a.N & 3) == 0;
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
             const int64_t t = t0 + j * 16 + row;
@@ -517,11 +677,10 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
 #pragma unroll
             for (int p = 0; p < NPW; ++p) {
                 const int n = (nw * NPW + p) * 16 + quarter * 4;
-                const f32x4 w = *(const f32x4*)(ws + n), c = *(const f32x4*)(bs + n);
                 float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = scaled(acc[p][j][e], as, w[e], c[e]);
-                store4(a.Y, a.out, t, n0 + n, a.N, vec, y);
+                for (int e = 0; e < 4; ++e) y[e] = scaled(acc[p][j][e], as, ws[n + e], bs[n + e]);
+                store_run<4>(a.Y, a.out, t, n0 + n, a.N, y);
             }
         }
     }
@@ -572,8 +731,35 @@ void embed_tiles(const LinearArgs& a, hipStream_t stream)
     else run_tiles<64, 1024, 1, 8, 64, 2, true, UNAL>(a, stream);
 }
 
+template <int KS, int NWV, int ST>
+void run_stream(LinearArgs a, hipStream_t stream)
+{
+    a.tiles_t = (int32_t)tiles(a.T, 32);
+    const int64_t most = (int64_t)device_cu_count() * (8 / NWV);  // 8 waves on each CU
+    hipLaunchKernelGGL((stream_kernel<KS, NWV, ST>), dim3((unsigned)(a.tiles_t < most ? a.tiles_t : most)),
+                       dim3(NWV * 64), 0, stream, a);
+}
+
+// The ring's stages: 72 KB a workgroup where two share a CU's LDS, 150 KB for one.
+bool stream_ok(const LinearArgs& a) { return a.N <= 256 && a.K <= 1024 && a.K % 128 == 0; }
+void embed_stream(const LinearArgs& a, hipStream_t stream)
+{
+    if (a.N <= 128) {
+        if (a.K <= 256) run_stream<8, 4, 6>(a, stream);
+        else if (a.K <= 512) run_stream<16, 4, 4>(a, stream);
+        else if (a.K <= 768) run_stream<24, 4, 3>(a, stream);
+        else run_stream<32, 4, 2>(a, stream);
+    } else {
+        if (a.K <= 256) run_stream<8, 8, 6>(a, stream);
+        else if (a.K <= 512) run_stream<16, 8, 6>(a, stream);
+        else if (a.K <= 768) run_stream<24, 8, 5>(a, stream);
+        else run_stream<32, 8, 4>(a, stream);
+    }
+}
+
 void embed_once(const LinearArgs& a, hipStream_t stream)
 {
+    if (a.T > 4096 && stream_ok(a)) return embed_stream(a, stream);
     if (a.T <= 4096) {
         if (a.N <= 128) run_few<1, 1, 8, 2, true>(a, stream);
         else if (a.N <= 256) run_few<1, 1, 16, 1, true>(a, stream);

@@ -274,13 +274,16 @@ EMBED = [
     (4500, 48, 300), (5000, 96, 77), (4200, 200, 256), (6000, 256, 400), (4300, 300, 96),
     (4100, 512, 1040), (4099, 513, 64), (5001, 1024, 320), (4098, 770, 130), (4200, 5, 33),
     (4120, 384, 72),
+    # many tokens, a projection that stays in registers: every depth and width class
+    (5000, 96, 128), (4999, 128, 384), (9000, 40, 640), (4111, 128, 1024), (40000, 128, 768),
+    (4500, 130, 256), (4100, 256, 512), (9001, 250, 896), (5003, 200, 768), (20000, 256, 1024),
 ]
 
 
 @pytest.mark.parametrize("T,d,K", EMBED)
 def test_embed(ms, T, d, K):
     a, s, w, ws, b = _operands(T, d, K, T + 2 * d + K)
-    m = _mask(T, d)
+    m = torch.cat([torch.ones(T % 4, dtype=torch.uint8, device=DEV), _mask(T, d)])[T % 4:]  # any byte address
     s = torch.where(m != 0, s, float("nan"))  # what masked rows hold does not matter
     live = f64(m) != 0
     y64, p64 = ref.linear(a.cpu().numpy(), np.where(live, f64(s), 0.0), w.cpu().numpy(), f64(ws), f64(b))
