@@ -35,8 +35,9 @@ __device__ __forceinline__ uint32_t half_bits(int out, float v)
                         : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// 16 bytes of a row of K bytes from byte k on; bytes past the row's end are 0.
-// UNAL: the row may start at any byte address.
+// 16 bytes of a row of K bytes from byte k on (k a multiple of 16); bytes past
+// the row's end are 0. UNAL: the row may start at any byte address. Only bytes
+// of the row are read.
 template <bool UNAL>
 __device__ __forceinline__ i32x4 load16(const int8_t* row, int k, int K)
 {
@@ -47,10 +48,19 @@ __device__ __forceinline__ i32x4 load16(const int8_t* row, int k, int K)
             const i32x4_any v = *(const i32x4_any*)(row + k);
             return i32x4{v[0], v[1], v[2], v[3]};
         }
+        if (k >= K) return i32x4{};
+        if (K >= 16) {
+            // the row's last 16 bytes, moved down by the bytes that lie before k
+            const i32x4_any v = *(const i32x4_any*)(row + K - 16);
+            unsigned __int128 x = (unsigned __int128)(((uint64_t)(uint32_t)v[3] << 32) | (uint32_t)v[2]) << 64 |
+                                  (((uint64_t)(uint32_t)v[1] << 32) | (uint32_t)v[0]);
+            x >>= 8 * (k + 16 - K);
+            return i32x4{(int)(uint32_t)x, (int)(uint32_t)(x >> 32), (int)(uint32_t)(x >> 64), (int)(uint32_t)(x >> 96)};
+        }
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (k + i < K) w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
+        for (int i = 0; i < 15; ++i)
+            if (i < K) w[i / 4] |= (uint32_t)(uint8_t)row[i] << (8 * (i % 4));
         return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
     }
 }
@@ -409,27 +419,36 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
         }
     }
     // The rest of k (all of it when rows are not 16-byte aligned) goes through
-    // registers, which fill up with zeros past the end of a row.
+    // registers, which fill up with zeros past the end of a row. The loads of one
+    // stage fly while the stage before it is multiplied.
     constexpr int kChunks = ((BT + BN) * C::kCpr + C::kThreads - 1) / C::kThreads;
-    for (int k0 = nk * KB; k0 < a.K; k0 += KB) {
-        i32x4 part[kChunks];
+    const int8_t* src[kChunks];
+    int chunk[kChunks], to[kChunks];
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int c = j * C::kThreads + threadIdx.x, r = c / C::kCpr;
-            const bool isA = r < BT;
-            const int local = isA ? r : channel_of(r - BT), last = (isA ? rows_t : rows_n) - 1;
-            if (r < BT + BN)
-                part[j] = load16<UNAL>((isA ? A : W) + (int64_t)(local < last ? local : last) * a.K,
-                                       k0 + c % C::kCpr * 16, a.K);
-        }
-        __syncthreads();  // the stage's last readers are done
+    for (int j = 0; j < kChunks; ++j) {
+        const int c = j * C::kThreads + threadIdx.x, r = c / C::kCpr;
+        const bool isA = r < BT;
+        const int local = isA ? r : channel_of(r - BT), last = (isA ? rows_t : rows_n) - 1;
+        src[j] = (isA ? A : W) + (int64_t)(local < last ? local : last) * a.K;
+        chunk[j] = c % C::kCpr * 16;
+        to[j] = r < BT + BN ? r * KB + place<KB>(r, c % C::kCpr) * 16 : -1;
+    }
+    i32x4 part[kChunks];
+    auto fetch = [&](int k0) {
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int c = j * C::kThreads + threadIdx.x, r = c / C::kCpr;
-            if (r < BT + BN) *(i32x4*)(ring + r * KB + place<KB>(r, c % C::kCpr) * 16) = part[j];
-        }
-        __syncthreads();
-        multiply<C, KB>(ring, w_row, a_row, acc);
+        for (int j = 0; j < kChunks; ++j)
+            if (to[j] >= 0) part[j] = load16<UNAL>(src[j], k0 + chunk[j], a.K);
+    };
+    if (nk * KB < a.K) fetch(nk * KB);
+    for (int k0 = nk * KB, i = nk; k0 < a.K; k0 += KB, ++i) {
+        if (i == nk) __syncthreads();  // the last readers of the direct stages are done
+        uint8_t* buf = ring + (i & 1) * C::kStage;
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j)
+            if (to[j] >= 0) *(i32x4*)(buf + to[j]) = part[j];
+        if (k0 + KB < a.K) fetch(k0 + KB);
+        block_barrier();  // stage i is written; stage i - 1, the other buffer, is read
+        multiply<C, KB>(buf, w_row, a_row, acc);
     }
     __syncthreads();  // ws and bs are written
 
@@ -716,7 +735,7 @@ void linear_once(const LinearArgs& a, hipStream_t stream)
     if (a.T <= 16) run_few<1, 1, 1, 8, false>(a, stream);
     else if (a.T <= 32) run_few<2, 1, 1, 8, false>(a, stream);
     else if (a.T <= 64) run_few<4, 1, 1, 8, false>(a, stream);
-    else if (unal) run_tiles<128, 128, 2, 2, 128, 2, false, true>(a, stream);
+    else if (unal) run_tiles<64, 64, 2, 2, 128, 2, false, true>(a, stream);
     else if (tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 128, 2, false, false>(a, stream);
     else if (tiles(a.T, 128) * tiles(a.N, 128) >= cus) run_tiles<128, 128, 2, 2, 128, 2, false, false>(a, stream);
     else run_tiles<64, 64, 2, 2, 128, 4, false, false>(a, stream);

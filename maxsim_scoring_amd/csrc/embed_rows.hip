@@ -100,10 +100,10 @@ __device__ __forceinline__ float dpp_f(float x)
 template <int G, typename OP>
 __device__ __forceinline__ float group_reduce(float v, OP op)
 {
-    static_assert(G == 8 || G == 16 || G == 32 || G == 64, "lanes per row");
-    v = op(v, dpp_f<0xB1>(v));   // quad_perm [1,0,3,2]
-    v = op(v, dpp_f<0x4E>(v));   // quad_perm [2,3,0,1]
-    v = op(v, dpp_f<0x141>(v));  // row_half_mirror
+    static_assert(G == 4 || G == 8 || G == 16 || G == 32 || G == 64, "lanes per row");
+    v = op(v, dpp_f<0xB1>(v));  // quad_perm [1,0,3,2]
+    v = op(v, dpp_f<0x4E>(v));  // quad_perm [2,3,0,1]
+    if constexpr (G >= 8) v = op(v, dpp_f<0x141>(v));   // row_half_mirror
     if constexpr (G >= 16) v = op(v, dpp_f<0x140>(v));  // row_mirror
     if constexpr (G >= 32) v = op(v, shfl_xor_f(v, 16));
     if constexpr (G >= 64) v = op(v, shfl_xor_f(v, 32));
@@ -116,34 +116,57 @@ struct Max { __device__ __forceinline__ float operator()(float a, float b) const
 // Quantisation
 // ---------------------------------------------------------------------------
 
-// Codes of C values of a row with largest magnitude top, inv = 127 / top;
-// returns the sum of squares of 127 x / top.
+// What the codes of a row need beside its values.
+struct Quant {
+    float top;   // largest magnitude
+    float inv;   // about 127 / top
+    float near;  // how far from an integer a code is decided in float64
+    bool zero;
+};
+__device__ __forceinline__ Quant quant_of(float top)
+{
+    Quant s;
+    s.top = top;
+    s.zero = !(top >= kTiny);
+    s.inv = s.zero ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(top);
+    s.near = top < 0x1p120f ? 0.5f - 0x1p-14f : -1.0f;  // the reciprocal of larger ones vanishes
+    return s;
+}
+
+// Codes of C values of a row; adds the squares of 127 x / top to ss.
 //
-// In float32 v = x * inv is within 127 * 2^-23 < 2^-15 of 127 x / top (inv and
-// the product are each off by 2^-24 relative). So the nearest integer to v is
-// the nearest to the quotient unless v is that close to the middle between two
-// integers; then the quotient is formed in float64. There it is a fraction of
-// two numbers of 24 and 31 bits: it is exactly a half, or further from one than
-// 2^-26, so a correctly rounded division (2^-46) decides it. The slow branch is
-// taken for about one chunk of 8 in 1,000.
-template <int C>
-__device__ __forceinline__ float make_codes(const float (&x)[C], float inv, float top, uint32_t (&w)[(C + 3) / 4])
+// v = x * inv is within 127 * 2^-22 = 2^-15 of 127 x / top (the reciprocal is
+// off by 2^-23 relative, two products by 2^-24 each). So the nearest integer to
+// v is the nearest to the quotient unless v is that close to the middle between
+// two integers; then the quotient is formed in float64. There it is a fraction
+// of two numbers of 31 and 24 bits: it is exactly a half, or further from one
+// than 2^-26, so a correctly rounded division (2^-46) decides it. The slow
+// branch is taken for about one chunk of 8 in 1,000.
+template <int C, bool SQUARES>
+__device__ __forceinline__ void make_codes(const float (&x)[C], const Quant& s, float& ss, uint32_t (&w)[(C + 3) / 4])
 {
     constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the integer, ties to even
     uint32_t b[C];
-    float off = 0.0f, ss = 0.0f;
+    float off = 0.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const float v = x[i] * inv;
+        const float v = x[i] * s.inv;
         const float m = v + kMagic;
         b[i] = __builtin_bit_cast(uint32_t, m);
         off = __builtin_fmaxf(off, __builtin_fabsf(v - (m - kMagic)));
-        ss = __builtin_fmaf(v, v, ss);
+        if (SQUARES) ss = __builtin_fmaf(v, v, ss);
     }
-    if (off >= 0.5f - 0x1p-14f) {
+    if (off >= s.near && !s.zero) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
-            b[i] = (uint32_t)(int)__builtin_rint((double)x[i] * 127.0 / (double)top);
+            b[i] = (uint32_t)(int)__builtin_rint((double)x[i] * 127.0 / (double)s.top);
+        if (SQUARES && s.near < 0.0f) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const float v = (float)((double)x[i] * 127.0 / (double)s.top);
+                ss = __builtin_fmaf(v, v, ss);
+            }
+        }
     }
     if constexpr (C == 1) {
         w[0] = b[0];
@@ -155,7 +178,6 @@ __device__ __forceinline__ float make_codes(const float (&x)[C], float inv, floa
             w[i] = lo | hi << 16;
         }
     }
-    return ss;
 }
 
 template <int C>
@@ -167,13 +189,17 @@ __device__ __forceinline__ void store_codes(void* Y, int64_t at, const uint32_t 
     else *(u32x2*)p = u32x2{w[0], w[1]};
 }
 
-__device__ __forceinline__ float quant_scale(int normalize, float ss, float top)
+// top / 127: the product with 1/127 and one correction step; or 1 / sqrt(ss).
+__device__ __forceinline__ float quant_scale(const Quant& s, bool normalize, float ss)
 {
-    return normalize ? 1.0f / __builtin_sqrtf(ss) : top / 127.0f;
+    if (s.zero) return 1.0f;
+    if (normalize) return __builtin_amdgcn_rsqf(ss);
+    const float q = s.top * (1.0f / 127.0f);
+    return __builtin_fmaf(__builtin_fmaf(-q, 127.0f, s.top), 1.0f / 127.0f, q);
 }
 
-template <int E, int VB, int G, int VPL>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(RowArgs a)
+template <int E, int VB, int G, int VPL, bool NORM>
+__device__ __forceinline__ void quantize_rows(const RowArgs& a)
 {
     constexpr int C = VB / elem_bytes<E>();
     typedef typename Raw<VB>::T R;
@@ -194,21 +220,25 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(RowArgs a)
 #pragma unroll
             for (int i = 0; i < C; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(x[i]));
         }
-        top = group_reduce<G>(top, Max{});
-        const bool zero = !(top >= kTiny);
-        const float inv = zero ? 0.0f : 127.0f / top;
+        const Quant s = quant_of(group_reduce<G>(top, Max{}));
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             float x[C];
             uint32_t w[(C + 3) / 4];
             unpack<E, VB>(raw[j], x);
-            ss += make_codes<C>(x, inv, top, w);
+            make_codes<C, NORM>(x, s, ss, w);
             if (lane + j * G < nv) store_codes<C>(a.Y, row * a.d + (int64_t)(lane + j * G) * C, w);
         }
-        ss = group_reduce<G>(ss, Add{});
-        if (lane == 0) a.stat[row] = zero ? 1.0f : quant_scale(a.normalize, ss, top);
+        if (NORM) ss = group_reduce<G>(ss, Add{});
+        if (lane == 0) a.stat[row] = quant_scale(s, NORM, ss);
     }
+}
+template <int E, int VB, int G, int VPL>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(RowArgs a)
+{
+    if (a.normalize) quantize_rows<E, VB, G, VPL, true>(a);
+    else quantize_rows<E, VB, G, VPL, false>(a);
 }
 
 // Rows longer than the register forms hold: one wave per row, read twice.
@@ -233,20 +263,18 @@ __global__ __launch_bounds__(kThreads) void quantize_long_kernel(RowArgs a)
                 for (int i = 0; i < C; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(x[i]));
             }
         }
-        top = group_reduce<64>(top, Max{});
-        const bool zero = !(top >= kTiny);
-        const float inv = zero ? 0.0f : 127.0f / top;
+        const Quant s = quant_of(group_reduce<64>(top, Max{}));
         float ss = 0.0f;
 #pragma unroll 4
         for (int c = lane; c < nv; c += 64) {
             float x[C];
             uint32_t w[(C + 3) / 4];
             unpack<E, VB>(live ? src[c] : R{}, x);
-            ss += make_codes<C>(x, inv, top, w);
+            make_codes<C, true>(x, s, ss, w);
             store_codes<C>(a.Y, row * a.d + (int64_t)c * C, w);
         }
         ss = group_reduce<64>(ss, Add{});
-        if (lane == 0) a.stat[row] = zero ? 1.0f : quant_scale(a.normalize, ss, top);
+        if (lane == 0) a.stat[row] = quant_scale(s, a.normalize != 0, ss);
     }
 }
 
@@ -301,7 +329,7 @@ __global__ __launch_bounds__(kThreads) void normalize_fwd_kernel(RowArgs a)
             }
             ss = group_reduce<G>(ss, Add{});
         }
-        const float r = 1.0f / __builtin_sqrtf(ss);
+        const float r = __builtin_amdgcn_rsqf(ss);
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             float x[C];
@@ -353,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void normalize_fwd_long_kernel(RowArgs a)
             }
             ss = group_reduce<64>(ss, Add{});
         }
-        const float r = 1.0f / __builtin_sqrtf(ss);
+        const float r = __builtin_amdgcn_rsqf(ss);
 #pragma unroll 4
         for (int c = lane; c < nv; c += 64) {
             float x[C];
@@ -552,14 +580,20 @@ unsigned row_blocks(int64_t T, int rows)
     return (unsigned)(b < kMaxBlocks ? b : kMaxBlocks);
 }
 
-// Picks the lanes per row and chunks per lane from the number of chunks.
-#define MAXSIM_ROWS(KERNEL, LONG, E, VB, MAXV)                                                                \
+// Picks the lanes per row and chunks per lane from the number of chunks; V
+// chunks per lane in the narrow classes. Quantisation's work per row (its
+// reduction, reciprocal and scale) is as long as that of a chunk, so two chunks
+// share it: 360,000 rows of 128 fp16 values take 21.4 us with 8 lanes x 2 chunks,
+// 42.4 with 16 x 1 and 23.7 with 4 x 4; normalisation of 131,072 such rows 11.0,
+// 11.4 and 11.0 us; its gradient, with 48 bytes to load per chunk, 23.7, 23.1
+// and 24.4 us.
+#define MAXSIM_ROWS(KERNEL, LONG, E, VB, V, MAXV)                                                            \
     do {                                                                                                     \
         const int nv = a.d / (VB / elem_bytes<E>());                                                          \
-        if (nv <= 8) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 8, 1);                                                  \
-        else if (nv <= 16) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 16, 1);                                           \
-        else if (nv <= 32) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 32, 1);                                           \
-        else if (nv <= 64) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 64, 1);                                           \
+        if (nv <= 8) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 8 / V, V);                                              \
+        else if (nv <= 16) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 16 / V, V);                                       \
+        else if (nv <= 32) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 32 / V, V);                                       \
+        else if (nv <= 64) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 64 / V, V);                                       \
         else if (nv <= 128) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 64, 2);                                          \
         else if (nv <= 256) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 64, 4);                                          \
         else if (nv <= 512) MAXSIM_ROW_LAUNCH(KERNEL, E, VB, 64, 8);                                          \
@@ -568,17 +602,17 @@ unsigned row_blocks(int64_t T, int rows)
     } while (0)
 #define MAXSIM_ROW_LAUNCH(KERNEL, E, VB, G, VPL) \
     hipLaunchKernelGGL((KERNEL<E, VB, G, VPL>), dim3(row_blocks(a.T, kThreads / (G))), dim3(kThreads), 0, stream, a)
-#define MAXSIM_ROW_TYPES(KERNEL, LONG, MAXV)                                             \
+#define MAXSIM_ROW_TYPES(KERNEL, LONG, V, MAXV)                                          \
     do {                                                                                 \
         if (elem == kF32) {                                                              \
-            if (a.d % 4 == 0) MAXSIM_ROWS(KERNEL, LONG, kF32, 16, MAXV);                 \
-            else MAXSIM_ROWS(KERNEL, LONG, kF32, 4, MAXV);                               \
+            if (a.d % 4 == 0) MAXSIM_ROWS(KERNEL, LONG, kF32, 16, V, MAXV);                 \
+            else MAXSIM_ROWS(KERNEL, LONG, kF32, 4, V, MAXV);                               \
         } else if (elem == kBF16) {                                                      \
-            if (a.d % 8 == 0) MAXSIM_ROWS(KERNEL, LONG, kBF16, 16, MAXV);                \
-            else MAXSIM_ROWS(KERNEL, LONG, kBF16, 2, MAXV);                              \
+            if (a.d % 8 == 0) MAXSIM_ROWS(KERNEL, LONG, kBF16, 16, V, MAXV);                \
+            else MAXSIM_ROWS(KERNEL, LONG, kBF16, 2, V, MAXV);                              \
         } else {                                                                         \
-            if (a.d % 8 == 0) MAXSIM_ROWS(KERNEL, LONG, kF16, 16, MAXV);                 \
-            else MAXSIM_ROWS(KERNEL, LONG, kF16, 2, MAXV);                               \
+            if (a.d % 8 == 0) MAXSIM_ROWS(KERNEL, LONG, kF16, 16, V, MAXV);                 \
+            else MAXSIM_ROWS(KERNEL, LONG, kF16, 2, V, MAXV);                               \
         }                                                                                \
     } while (0)
 
@@ -586,19 +620,19 @@ unsigned row_blocks(int64_t T, int rows)
 
 hipError_t launch_quantize(int elem, RowArgs a, hipStream_t stream)
 {
-    MAXSIM_ROW_TYPES(quantize_kernel, quantize_long_kernel, 16);
+    MAXSIM_ROW_TYPES(quantize_kernel, quantize_long_kernel, 2, 16);
     return hipGetLastError();
 }
 
 hipError_t launch_normalize_fwd(int elem, RowArgs a, hipStream_t stream)
 {
-    MAXSIM_ROW_TYPES(normalize_fwd_kernel, normalize_fwd_long_kernel, 16);
+    MAXSIM_ROW_TYPES(normalize_fwd_kernel, normalize_fwd_long_kernel, 2, 16);
     return hipGetLastError();
 }
 
 hipError_t launch_normalize_bwd(int elem, RowArgs a, hipStream_t stream)
 {
-    MAXSIM_ROW_TYPES(normalize_bwd_kernel, normalize_bwd_long_kernel, 8);
+    MAXSIM_ROW_TYPES(normalize_bwd_kernel, normalize_bwd_long_kernel, 1, 8);
     return hipGetLastError();
 }
 
