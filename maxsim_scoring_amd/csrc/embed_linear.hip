@@ -468,6 +468,42 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
         embed_rows<C::TT, C::NT, 16, 32, WN>(
             a, [&](auto j, auto b, int i) { return acc[b][j][i]; },
             [&](int b) { return (wn * C::NT + b) * 32 + half * 16; }, ws, bs, t, as, live, slot, wn, red, BT);
+    } else if (a.N & 3) {
+        // Rows at any address: the wave turns its 32 tokens x NT * 32 channels
+        // through its part of the ring, so that lanes store neighbouring channels
+        // (1213 x 1001 float32 outputs of K = 1000: 11.9 us, 16.3 with every lane
+        // storing its own run value by value).
+        constexpr int kCols = C::NT * 32, kStride = kCols + 4;
+        static_assert(C::kWaves * 32 * kStride * 4 <= ST * C::kStage, "the ring holds the outputs");
+        float* mine = (float*)ring + wave * 32 * kStride;
+        const int n_base = wn * kCols;
+#pragma unroll
+        for (int j = 0; j < C::TT; ++j) {
+            const int64_t tile = t0 + a_row + j * 32, t = tile + (lane & 31);
+            const float as = t < a.T ? a.a_scale[t] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int n = i * 32 + half * 16 + e;
+                    mine[(lane & 31) * kStride + n] = scaled(acc[i][j][e], as, ws[n_base + n], bs[n_base + n]);
+                }
+            lds_fence();
+            constexpr int kPer = kCols < 64 ? 64 / kCols : 1;  // rows per step
+            const int col = lane % (kCols < 64 ? kCols : 64), sub = lane / (kCols < 64 ? kCols : 64);
+            for (int r = sub; r < 32 && tile + r < a.T; r += kPer) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 64) {
+                    const int n = n_base + c + col;
+                    if (n >= rows_n) continue;
+                    const float y = mine[r * kStride + c + col];
+                    const int64_t at = (tile + r) * a.N + n0 + n;
+                    if (a.out == kF32) ((float*)a.Y)[at] = y;
+                    else ((uint16_t*)a.Y)[at] = (uint16_t)half_bits(a.out, y);
+                }
+            }
+            lds_fence();
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < C::TT; ++j) {
@@ -735,6 +771,8 @@ void linear_once(const LinearArgs& a, hipStream_t stream)
     if (a.T <= 16) run_few<1, 1, 1, 8, false>(a, stream);
     else if (a.T <= 32) run_few<2, 1, 1, 8, false>(a, stream);
     else if (a.T <= 64) run_few<4, 1, 1, 8, false>(a, stream);
+    else if (unal && tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 128, 2, false, true>(a, stream);
+    else if (unal && tiles(a.T, 128) * tiles(a.N, 128) >= 2 * cus) run_tiles<128, 128, 2, 2, 128, 2, false, true>(a, stream);
     else if (unal) run_tiles<64, 64, 2, 2, 128, 2, false, true>(a, stream);
     else if (tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 128, 2, false, false>(a, stream);
     else if (tiles(a.T, 128) * tiles(a.N, 128) >= cus) run_tiles<128, 128, 2, 2, 128, 2, false, false>(a, stream);
