@@ -11,6 +11,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -558,28 +559,35 @@ class _On:
     current, so the call launches there and the outputs it allocates belong to
     that stream."""
 
-    def __init__(self, stream, **tensors):
-        dev = None
-        for name, t in tensors.items():
+    __slots__ = ("_ctx", "handle")
+
+    def __init__(self, stream, tensors):
+        dev = tensors[0][1].device
+        for name, t in tensors:
             if t is None:
                 continue
-            _dev(name, t)
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a GPU tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.device != dev:
                 raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream must be one of {dev}, got {stream.device}")
-        self.device = dev
-        self._stream = stream
         self._ctx = None
+        if stream is None:
+            # the raw handle: building a Stream object takes longer than the checks
+            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
+            if dev.index != torch._C._cuda_getDevice():
+                self._ctx = torch.cuda.device(dev)
+        else:
+            if stream.device != dev:
+                raise ValueError(f"stream must be one of {dev}, got {stream.device}")
+            self.handle = stream.cuda_stream
+            self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.device.index != torch.cuda.current_device() or self._stream is not None:
-            self._ctx = torch.cuda.stream(self._stream if self._stream is not None
-                                          else torch.cuda.current_stream(self.device))
+        if self._ctx is not None:
             self._ctx.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+        return self.handle
 
     def __exit__(self, *exc):
         if self._ctx is not None:
@@ -587,15 +595,20 @@ class _On:
         return False
 
 
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _has(name: str, t: Optional[torch.Tensor], dtype, shape) -> None:
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
 def _rows(name: str, t: torch.Tensor):
     """(leading shape, rows, width) of a tensor of rows."""
     if t.dim() < 1:
         raise ValueError(f"{name} must have rows in its last dimension")
-    lead = tuple(t.shape[:-1])
-    rows = 1
-    for n in lead:
-        rows *= n
-    return lead, rows, t.shape[-1]
+    return t.shape[:-1], math.prod(t.shape[:-1]), t.shape[-1]
 
 
 def maxsim_quantize_tok(X: torch.Tensor, mask: Optional[torch.Tensor] = None,
@@ -607,17 +620,17 @@ def maxsim_quantize_tok(X: torch.Tensor, mask: Optional[torch.Tensor] = None,
     of zeros) get codes 0, scale 1. Returns (codes int8 [..., d], scale float32 [...])."""
     code = _row_type("X", X.dtype)
     lead, T, d = _rows("X", X)
-    _mask("mask", mask, lead)
-    with _On(stream, X=X, mask=mask, codes=codes, scale=scale) as st:
+    _has("mask", mask, torch.uint8, lead)
+    _has("codes", codes, torch.int8, X.shape)
+    _has("scale", scale, torch.float32, lead)
+    with _On(stream, (("X", X), ("mask", mask), ("codes", codes), ("scale", scale))) as st:
         if codes is None:
-            codes = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+            codes = torch.empty_like(X, dtype=torch.int8)
         if scale is None:
             scale = torch.empty(lead, dtype=torch.float32, device=X.device)
-        _out("codes", codes, torch.int8, X.shape)
-        _out("scale", scale, torch.float32, lead)
         _check("maxsim_quantize_tok",
-               lib().maxsim_quantize_tok(code, _p(X), T, d, _p(mask), int(bool(normalize)),
-                                         _p(codes), _p(scale), st))
+               lib().maxsim_quantize_tok(code, X.data_ptr(), T, d, _at(mask), bool(normalize),
+                                         codes.data_ptr(), scale.data_ptr(), st))
     return codes, scale
 
 
@@ -626,10 +639,11 @@ def _linear_args(A, a_scale, W, w_scale, bias):
     if W.dim() != 2 or W.shape[1] != K:
         raise ValueError(f"W must be [N, {K}], got {list(W.shape)}")
     N = W.shape[0]
-    _dev("A", A, torch.int8)
-    _dev("W", W, torch.int8)
-    for name, t, shape in (("a_scale", a_scale, lead), ("w_scale", w_scale, (N,)), ("bias", bias, (N,))):
-        _out(name, t, torch.float32, shape)
+    if A.dtype != torch.int8 or W.dtype != torch.int8:
+        raise ValueError("A and W must be int8")
+    _has("a_scale", a_scale, torch.float32, lead)
+    _has("w_scale", w_scale, torch.float32, (N,))
+    _has("bias", bias, torch.float32, (N,))
     return lead, T, K, N
 
 
@@ -641,13 +655,15 @@ def maxsim_linear_i8(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
     of ``out_dtype`` (fp16, bf16 or fp32)."""
     lead, T, K, N = _linear_args(A, a_scale, W, w_scale, bias)
     code = _row_type("out_dtype", out_dtype if Y is None else Y.dtype)
-    with _On(stream, A=A, a_scale=a_scale, W=W, w_scale=w_scale, bias=bias, Y=Y) as st:
+    if Y is not None:
+        _has("Y", Y, Y.dtype, lead + (N,))
+    with _On(stream, (("A", A), ("a_scale", a_scale), ("W", W), ("w_scale", w_scale),
+                      ("bias", bias), ("Y", Y))) as st:
         if Y is None:
             Y = torch.empty(lead + (N,), dtype=out_dtype, device=A.device)
-        _out("Y", Y, Y.dtype, lead + (N,))
         _check("maxsim_linear_i8",
-               lib().maxsim_linear_i8(code, _p(A), _p(a_scale), _p(W), _p(w_scale), _p(bias), T, N,
-                                      K, _p(Y), st))
+               lib().maxsim_linear_i8(code, A.data_ptr(), a_scale.data_ptr(), W.data_ptr(),
+                                      w_scale.data_ptr(), _at(bias), T, N, K, Y.data_ptr(), st))
     return Y
 
 
@@ -662,22 +678,23 @@ def maxsim_embed_i8(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
     [...]: masked rows give zeros (codes 0, scale 1). Returns (E [..., d],
     e_scale float32 [...] or None)."""
     lead, T, K, d = _linear_args(A, a_scale, W, w_scale, bias)
-    _mask("mask", mask, lead)
+    _has("mask", mask, torch.uint8, lead)
     dt = out_dtype if E is None else E.dtype
     code = MAXSIM_I8 if dt == torch.int8 else _row_type("out_dtype", dt)
     if code != MAXSIM_I8 and e_scale is not None:
         raise ValueError("e_scale is an output of int8 embeddings only")
-    with _On(stream, A=A, a_scale=a_scale, W=W, w_scale=w_scale, bias=bias, mask=mask, E=E,
-             e_scale=e_scale) as st:
+    _has("E", E, dt, lead + (d,))
+    _has("e_scale", e_scale, torch.float32, lead)
+    with _On(stream, (("A", A), ("a_scale", a_scale), ("W", W), ("w_scale", w_scale),
+                      ("bias", bias), ("mask", mask), ("E", E), ("e_scale", e_scale))) as st:
         if E is None:
             E = torch.empty(lead + (d,), dtype=dt, device=A.device)
         if e_scale is None and code == MAXSIM_I8:
             e_scale = torch.empty(lead, dtype=torch.float32, device=A.device)
-        _out("E", E, dt, lead + (d,))
-        _out("e_scale", e_scale, torch.float32, lead)
         _check("maxsim_embed_i8",
-               lib().maxsim_embed_i8(code, _p(A), _p(a_scale), _p(W), _p(w_scale), _p(bias),
-                                     _p(mask), T, d, K, _p(E), _p(e_scale), st))
+               lib().maxsim_embed_i8(code, A.data_ptr(), a_scale.data_ptr(), W.data_ptr(),
+                                     w_scale.data_ptr(), _at(bias), _at(mask), T, d, K,
+                                     E.data_ptr(), _at(e_scale), st))
     return E, e_scale
 
 
@@ -702,16 +719,17 @@ def maxsim_normalize_fwd(X: torch.Tensor, mask: Optional[torch.Tensor] = None, o
     dt = Y.dtype if Y is not None else X.dtype if out_dtype is None else out_dtype
     yt = _row_type("out_dtype", dt)
     lead, T, d = _rows("X", X)
-    _mask("mask", mask, lead)
-    with _On(stream, X=X, mask=mask, Y=Y, rnorm=rnorm) as st:
+    _has("mask", mask, torch.uint8, lead)
+    _has("Y", Y, dt, X.shape)
+    _has("rnorm", rnorm, torch.float32, lead)
+    with _On(stream, (("X", X), ("mask", mask), ("Y", Y), ("rnorm", rnorm))) as st:
         if Y is None:
-            Y = torch.empty(X.shape, dtype=dt, device=X.device)
+            Y = torch.empty_like(X, dtype=dt)
         if rnorm is None:
             rnorm = torch.empty(lead, dtype=torch.float32, device=X.device)
-        _out("Y", Y, dt, X.shape)
-        _out("rnorm", rnorm, torch.float32, lead)
         _check("maxsim_normalize_fwd",
-               lib().maxsim_normalize_fwd(xt, _p(X), T, d, _p(mask), yt, _p(Y), _p(rnorm), st))
+               lib().maxsim_normalize_fwd(xt, X.data_ptr(), T, d, _at(mask), yt, Y.data_ptr(),
+                                          rnorm.data_ptr(), st))
     return Y, rnorm
 
 
@@ -724,14 +742,15 @@ def maxsim_normalize_bwd(X: torch.Tensor, rnorm: torch.Tensor, dY: torch.Tensor,
     dt = dX.dtype if dX is not None else X.dtype if out_dtype is None else out_dtype
     gt = _row_type("out_dtype", dt)
     lead, T, d = _rows("X", X)
-    with _On(stream, X=X, rnorm=rnorm, dY=dY, dX=dX) as st:
-        _out("rnorm", rnorm, torch.float32, lead)
-        _out("dY", dY, torch.float32, X.shape)
+    _has("rnorm", rnorm, torch.float32, lead)
+    _has("dY", dY, torch.float32, X.shape)
+    _has("dX", dX, dt, X.shape)
+    with _On(stream, (("X", X), ("rnorm", rnorm), ("dY", dY), ("dX", dX))) as st:
         if dX is None:
-            dX = torch.empty(X.shape, dtype=dt, device=X.device)
-        _out("dX", dX, dt, X.shape)
+            dX = torch.empty_like(X, dtype=dt)
         _check("maxsim_normalize_bwd",
-               lib().maxsim_normalize_bwd(xt, _p(X), _p(rnorm), _p(dY), T, d, gt, _p(dX), st))
+               lib().maxsim_normalize_bwd(xt, X.data_ptr(), rnorm.data_ptr(), dY.data_ptr(), T, d,
+                                          gt, dX.data_ptr(), st))
     return dX
 
 
@@ -740,14 +759,14 @@ def _dropout(fn: str, X, p, seed, step, step_dev, Y, stream, names):
     for name, v in (("seed", seed), ("step", step)):
         if not 0 <= int(v) < 1 << 64:
             raise ValueError(f"{name} must be in [0, 2^64), got {v}")
-    with _On(stream, **{names[0]: X, "step_dev": step_dev, names[1]: Y}) as st:
-        if step_dev is not None and (step_dev.dtype != torch.int64 or step_dev.numel() != 1):
-            raise ValueError("step_dev must be one int64")
+    if step_dev is not None and (step_dev.dtype != torch.int64 or step_dev.numel() != 1):
+        raise ValueError("step_dev must be one int64")
+    _has(names[1], Y, X.dtype, X.shape)
+    with _On(stream, ((names[0], X), ("step_dev", step_dev), (names[1], Y))) as st:
         if Y is None:
-            Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-        _out(names[1], Y, X.dtype, X.shape)
-        _check(fn, getattr(lib(), fn)(code, _p(X), X.numel(), float(p), int(seed), int(step),
-                                      _p(step_dev), _p(Y), st))
+            Y = torch.empty_like(X)
+        _check(fn, getattr(lib(), fn)(code, X.data_ptr(), X.numel(), float(p), int(seed), int(step),
+                                      _at(step_dev), Y.data_ptr(), st))
     return Y
 
 

@@ -202,7 +202,7 @@ __device__ __forceinline__ void join_rows(double (&top)[TT], double (&ss)[TT], d
 // of the workgroup's channels, 0 past the last one.
 //
 // With s the largest magnitude of the row, its values over the norm are
-// (y / s) * (s / ||y||), whose factors neither overflow nor vanish; the sum of
+// (y / s) / ||y / s||, whose factors neither overflow nor vanish; the sum of
 // squares is a float64, which holds the square of every float32 y. Codes are
 // the nearest integers to 127 y / s: y and s are float64 there, so that a value
 // next to the middle between two codes is not moved across it, and adding
@@ -246,7 +246,7 @@ __device__ __forceinline__ void embed_rows(const LinearArgs& a, GET get, CHAN ch
         if (a.out != kI8) {
             const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
             const float inv = 1.0f / (float)top[tt];
-            const float r = (float)(top[tt] / __builtin_sqrt(ss[tt]));
+            const float r = __builtin_amdgcn_rsqf((float)(ss[tt] * (double)inv * (double)inv));  // 1 .. N inside
             if (in) {
                 static_for<0, NB>([&](auto b) {
                     float y[R];
@@ -270,9 +270,9 @@ __device__ __forceinline__ void embed_rows(const LinearArgs& a, GET get, CHAN ch
                     }
                     store_codes<R>(a.Y, t[tt], chan(b), a.N, q);
                 });
-                // codes * scale is y / ||y||, so scale = s / (127 ||y||)
+                // codes * scale is y / ||y||, so scale = 1 / ||127 y / s||
                 if (wn == 0 && lane_id() < COLS)
-                    a.y_scale[t[tt]] = zero ? 1.0f : (float)(top[tt] / (127.0 * __builtin_sqrt(ss[tt])));
+                    a.y_scale[t[tt]] = zero ? 1.0f : __builtin_amdgcn_rsqf((float)(ss[tt] * inv * inv));
             }
         }
     });
@@ -286,7 +286,7 @@ __device__ __forceinline__ void embed_rows(const LinearArgs& a, GET get, CHAN ch
 template <int KB>
 __device__ __forceinline__ int place(int row, int c)
 {
-    if constexpr (KB == 128) return swz_chunk<128>(row, c);
+    if constexpr (KB >= 128) return swz_chunk<KB>(row, c);
     else return c ^ ((row >> 2) & 3);  // 64-byte rows: four share a 256-byte bank line
 }
 
@@ -311,6 +311,7 @@ struct Tile {
     static constexpr int kRows = 64 / kCpr;  // rows of one load
     static_assert(BT % kRows == 0 && BN % kRows == 0, "a load stays inside one operand");
     static_assert(ST == 2 || kLoads % kWaves == 0, "deep rings count their loads");
+    static_assert(EMBED || kWaves * 32 * (NT * 32 + 4) * 4 <= ST * kStage, "the ring holds a turned output");
 };
 
 // One stage's MFMAs: the wave's channels x tokens, KB bytes of k from `buf`.
@@ -333,6 +334,81 @@ __device__ __forceinline__ void multiply(const uint8_t* buf, int w_row, int a_ro
     }
 }
 
+// Writes a wave's NT x 32 channels of TT x 32 tokens of a linear product, from
+// channel n0 + wn * NT * 32 and token t0 + a_row on. ring: LDS of at least
+// 32 x (NT * 32 + 4) floats per wave, free to overwrite.
+template <int NT, int TT>
+__device__ __forceinline__ void store_tile(const LinearArgs& a, const i32x16 (&acc)[NT][TT], const float* ws,
+                                           const float* bs, int64_t t0, int n0, int a_row, int wn, int wave,
+                                           uint8_t* ring)
+{
+    const int lane = lane_id(), half = lane >> 5;
+    if (a.N & 3) {
+        // Rows at any address: the wave turns its tokens x channels through LDS, so
+        // that lanes store neighbouring channels (1213 x 1001 float32 outputs of
+        // K = 1000: 11.9 us, 16.3 with every lane storing its own run value by value).
+        constexpr int kCols = NT * 32, kStride = kCols + 4;
+        float* mine = (float*)ring + wave * 32 * kStride;
+        const int n_base = wn * kCols;
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const int64_t tile = t0 + a_row + j * 32, t = tile + (lane & 31);
+            const float as = t < a.T ? a.a_scale[t] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int n = i * 32 + half * 16 + e;
+                    mine[(lane & 31) * kStride + n] = scaled(acc[i][j][e], as, ws[n_base + n], bs[n_base + n]);
+                }
+            lds_fence();
+            constexpr int kStep = kCols < 64 ? kCols : 64, kPer = 64 / kStep;  // columns and rows per store
+            const int col = lane % kStep, sub = lane / kStep;
+            for (int r = sub; r < 32 && tile + r < a.T; r += kPer) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += kStep) {
+                    const int n = n0 + n_base + c + col;
+                    if (n >= a.N) continue;
+                    const float y = mine[r * kStride + c + col];
+                    const int64_t at = (tile + r) * a.N + n;
+                    if (a.out == kF32) ((float*)a.Y)[at] = y;
+                    else ((uint16_t*)a.Y)[at] = (uint16_t)half_bits(a.out, y);
+                }
+            }
+            lds_fence();
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int64_t t = t0 + a_row + j * 32 + (lane & 31);
+        if (t >= a.T) continue;
+        const float as = a.a_scale[t];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int n = (wn * NT + i) * 32 + half * 16;
+            float y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = scaled(acc[i][j][e], as, ws[n + e], bs[n + e]);
+            store_run<16>(a.Y, a.out, t, n0 + n, a.N, y);
+        }
+    }
+}
+
+// Workgroup to tile: consecutive workgroups go to the 8 XCDs in turn, so each XCD
+// takes a contiguous run of tiles, walked in bands of 8 token tiles, whose
+// operands the XCD's L2 then holds.
+__device__ __forceinline__ void tile_of(const LinearArgs& a, int BT, int BN, int64_t& t0, int& n0)
+{
+    const int nwg = a.tiles_t * a.tiles_n, b = blockIdx.x;
+    const int q = nwg >> 3, r = nwg & 7, x = b & 7;
+    const int id = x * q + (x < r ? x : r) + (b >> 3);
+    const int per = 8 * a.tiles_n, band = id / per, in = id - band * per;
+    const int left = a.tiles_t - band * 8, high = left < 8 ? left : 8;
+    t0 = (int64_t)(band * 8 + in % high) * BT;
+    n0 = in / high * BN;
+}
+
 template <int BT, int BN, int WT, int WN, int KB, int ST, bool EMBED, bool UNAL>
 __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
 {
@@ -344,20 +420,9 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int wt = wave / WN, wn = wave % WN;
 
-    // Workgroup to tile: consecutive workgroups go to the 8 XCDs in turn, so
-    // each XCD takes a contiguous run of tiles, walked in blocks of 8 token
-    // tiles, whose operands the XCD's L2 then holds.
     int64_t t0;
     int n0;
-    {
-        const int nwg = a.tiles_t * a.tiles_n, b = blockIdx.x;
-        const int q = nwg >> 3, r = nwg & 7, x = b & 7;
-        const int id = x * q + (x < r ? x : r) + (b >> 3);
-        const int per = 8 * a.tiles_n, band = id / per, in = id - band * per;
-        const int left = a.tiles_t - band * 8, high = left < 8 ? left : 8;
-        t0 = (int64_t)(band * 8 + in % high) * BT;
-        n0 = in / high * BN;
-    }
+    tile_of(a, BT, BN, t0, n0);
     const int rows_t = (int)(a.T - t0 < BT ? a.T - t0 : BT);
     const int rows_n = a.N - n0 < BN ? a.N - n0 : BN;
     const int8_t* A = a.A + t0 * a.K;
@@ -392,9 +457,15 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
     const int nk = UNAL ? 0 : a.K / KB;  // stages filled by direct-to-LDS loads
     if constexpr (!UNAL) {
         const uint32_t ring0 = lds_addr(ring);
+        // The order of k does not matter to whole numbers. Rows a multiple of 4 KB
+        // apart meet the same few memory channels at one k, so workgroups that read
+        // their hidden states from memory start at different ones (100,000 x 4096 to
+        // 128 channels 108 us, 121 without).
+        const int first = EMBED && (a.K & 4095) == 0 ? (int)(blockIdx.x % (unsigned)nk) : 0;
         auto issue = [&](int i) {
-            const int8_t* pa = A + (int64_t)i * KB;
-            const int8_t* pw = W + (int64_t)i * KB;
+            const int ki = first + i < nk ? first + i : first + i - nk;
+            const int8_t* pa = A + (int64_t)ki * KB;
+            const int8_t* pw = W + (int64_t)ki * KB;
             const uint32_t at = ring0 + (uint32_t)(i % ST) * C::kStage;
 #pragma unroll
             for (int j = 0; j < C::kPerWave; ++j) {
@@ -468,57 +539,8 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
         embed_rows<C::TT, C::NT, 16, 32, WN>(
             a, [&](auto j, auto b, int i) { return acc[b][j][i]; },
             [&](int b) { return (wn * C::NT + b) * 32 + half * 16; }, ws, bs, t, as, live, slot, wn, red, BT);
-    } else if (a.N & 3) {
-        // Rows at any address: the wave turns its 32 tokens x NT * 32 channels
-        // through its part of the ring, so that lanes store neighbouring channels
-        // (1213 x 1001 float32 outputs of K = 1000: 11.9 us, 16.3 with every lane
-        // storing its own run value by value).
-        constexpr int kCols = C::NT * 32, kStride = kCols + 4;
-        static_assert(C::kWaves * 32 * kStride * 4 <= ST * C::kStage, "the ring holds the outputs");
-        float* mine = (float*)ring + wave * 32 * kStride;
-        const int n_base = wn * kCols;
-#pragma unroll
-        for (int j = 0; j < C::TT; ++j) {
-            const int64_t tile = t0 + a_row + j * 32, t = tile + (lane & 31);
-            const float as = t < a.T ? a.a_scale[t] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < C::NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int n = i * 32 + half * 16 + e;
-                    mine[(lane & 31) * kStride + n] = scaled(acc[i][j][e], as, ws[n_base + n], bs[n_base + n]);
-                }
-            lds_fence();
-            constexpr int kPer = kCols < 64 ? 64 / kCols : 1;  // rows per step
-            const int col = lane % (kCols < 64 ? kCols : 64), sub = lane / (kCols < 64 ? kCols : 64);
-            for (int r = sub; r < 32 && tile + r < a.T; r += kPer) {
-#pragma unroll
-                for (int c = 0; c < kCols; c += 64) {
-                    const int n = n_base + c + col;
-                    if (n >= rows_n) continue;
-                    const float y = mine[r * kStride + c + col];
-                    const int64_t at = (tile + r) * a.N + n0 + n;
-                    if (a.out == kF32) ((float*)a.Y)[at] = y;
-                    else ((uint16_t*)a.Y)[at] = (uint16_t)half_bits(a.out, y);
-                }
-            }
-            lds_fence();
-        }
     } else {
-#pragma unroll
-        for (int j = 0; j < C::TT; ++j) {
-            const int64_t t = t0 + a_row + j * 32 + (lane & 31);
-            if (t >= a.T) continue;
-            const float as = a.a_scale[t];
-#pragma unroll
-            for (int i = 0; i < C::NT; ++i) {
-                const int n = (wn * C::NT + i) * 32 + half * 16;
-                float y[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = scaled(acc[i][j][e], as, ws[n + e], bs[n + e]);
-                store_run<16>(a.Y, a.out, t, n0 + n, a.N, y);
-            }
-        }
+        store_tile<C::NT, C::TT>(a, acc, ws, bs, t0, n0, a_row, wn, wave, ring);
     }
 }
 
@@ -659,6 +681,15 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
         const int64_t t = t0 + j * 16 + row;
         ap[j] = a.A + (t < a.T ? t : a.T - 1) * a.K;
     }
+    float as[TT];  // loaded beside the first rows
+    bool live[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int64_t t = t0 + j * 16 + row;
+        const bool in = t < a.T && kw == 0;
+        as[j] = in ? a.a_scale[t] : 0.0f;
+        live[j] = in && (!EMBED || !a.mask || a.mask[t]);
+    }
     i32x4 acc[NPW][TT];
 #pragma unroll
     for (int p = 0; p < NPW; ++p)
@@ -709,14 +740,11 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
         // the waves of other k parts only keep the barriers: they hold no rows
         int64_t t[TT];
         int slot[TT];
-        float as[TT];
-        bool live[TT];
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
             slot[j] = j * 16 + row;
             t[j] = kw == 0 ? t0 + slot[j] : a.T;
-            live[j] = t[j] < a.T && (!a.mask || a.mask[t[j]]);
-            as[j] = live[j] ? a.a_scale[t[j]] : 0.0f;
+            if (!live[j]) as[j] = 0.0f;
         }
         embed_rows<TT, NPW, 4, 16, NW>(
             a, [&](auto j, auto b, int i) { return acc[b][j][i]; },
@@ -728,13 +756,12 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
         for (int j = 0; j < TT; ++j) {
             const int64_t t = t0 + j * 16 + row;
             if (t >= a.T) continue;
-            const float as = a.a_scale[t];
 #pragma unroll
             for (int p = 0; p < NPW; ++p) {
                 const int n = (nw * NPW + p) * 16 + quarter * 4;
                 float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = scaled(acc[p][j][e], as, ws[n + e], bs[n + e]);
+                for (int e = 0; e < 4; ++e) y[e] = scaled(acc[p][j][e], as[j], ws[n + e], bs[n + e]);
                 store_run<4>(a.Y, a.out, t, n0 + n, a.N, y);
             }
         }
@@ -764,27 +791,44 @@ void run_few(const LinearArgs& a, hipStream_t stream)
     else hipLaunchKernelGGL((few_kernel<TT, NPW, NW, KW, EMBED, true>), grid, block, 0, stream, a);
 }
 
-void linear_once(const LinearArgs& a, hipStream_t stream)
+// Tiles by how many the launch has (median us of N = K = 4096 bf16 outputs with
+// 256 x 256 / 128 x 128 / 64 x 128 / 64 x 64 tiles):
+//   T = 8192  122 / 134 / 167 / 207     2048   49 /  36 /  44 /  52
+//   T = 4096   62 /  68 /  85 / 100     1024   47 /  26 /  24 /  28
+//   T =  512   47 /  24 /  18 /  16       96   44 /  23 /  17 /  11
+// One 256 x 256 tile fills a CU, two or more of the smaller ones share it. Up to
+// 32 tokens the direct form is ahead (32 tokens 8.7 against 10.8 us, 16 6.5
+// against 10.8; 64 tokens 13.1 against 11.0).
+template <bool UNAL>
+void linear_tiles(const LinearArgs& a, hipStream_t stream)
 {
-    const int cus = device_cu_count();
-    const bool unal = a.K % 16 != 0;
-    if (a.T <= 16) run_few<1, 1, 1, 8, false>(a, stream);
-    else if (a.T <= 32) run_few<2, 1, 1, 8, false>(a, stream);
-    else if (a.T <= 64) run_few<4, 1, 1, 8, false>(a, stream);
-    else if (unal && tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 128, 2, false, true>(a, stream);
-    else if (unal && tiles(a.T, 128) * tiles(a.N, 128) >= 2 * cus) run_tiles<128, 128, 2, 2, 128, 2, false, true>(a, stream);
-    else if (unal) run_tiles<64, 64, 2, 2, 128, 2, false, true>(a, stream);
-    else if (tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 128, 2, false, false>(a, stream);
-    else if (tiles(a.T, 128) * tiles(a.N, 128) >= cus) run_tiles<128, 128, 2, 2, 128, 2, false, false>(a, stream);
-    else run_tiles<64, 64, 2, 2, 128, 4, false, false>(a, stream);
+    const int64_t cus = device_cu_count();
+    if (tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 128, 2, false, UNAL>(a, stream);
+    else if (tiles(a.T, 128) * tiles(a.N, 128) >= 2 * cus) run_tiles<128, 128, 2, 2, 128, 2, false, UNAL>(a, stream);
+    else if (!UNAL && tiles(a.T, 64) * tiles(a.N, 128) >= 2 * cus)
+        run_tiles<64, 128, 2, 2, 128, 3, false, false>(a, stream);
+    else run_tiles<64, 64, 2, 2, 128, UNAL ? 2 : 4, false, UNAL>(a, stream);
 }
 
+void linear_once(const LinearArgs& a, hipStream_t stream)
+{
+    if (a.T <= 16) run_few<1, 1, 1, 8, false>(a, stream);
+    else if (a.T <= 32) run_few<2, 1, 1, 8, false>(a, stream);
+    else if (a.K % 16 == 0) linear_tiles<false>(a, stream);
+    else linear_tiles<true>(a, stream);
+}
+
+// Every workgroup holds whole rows, so the tile's tokens shrink as the channels
+// grow. Up to 128 channels two workgroups of 128 tokens share a CU: 200,000 tokens
+// of 2048 to 128 channels take 115 us, 127 with one of 256 tokens, 149 with
+// 64-byte steps of k; to 256 channels 169 us with 256 tokens, 192 with 128.
 template <bool UNAL>
 void embed_tiles(const LinearArgs& a, hipStream_t stream)
 {
-    if (a.N <= 128) run_tiles<256, 128, 8, 1, 128, 2, true, UNAL>(a, stream);
-    else if (a.N <= 256) run_tiles<128, 256, 4, 2, 128, 2, true, UNAL>(a, stream);
+    if (a.N <= 128) run_tiles<128, 128, 4, 1, 128, 2, true, UNAL>(a, stream);
+    else if (a.N <= 256) run_tiles<256, 256, 4, 2, 128, 2, true, UNAL>(a, stream);
     else if (a.N <= 512) run_tiles<64, 512, 2, 4, 128, 2, true, UNAL>(a, stream);
+    else if (a.N <= 768) run_tiles<64, 768, 1, 8, 64, 2, true, UNAL>(a, stream);
     else run_tiles<64, 1024, 1, 8, 64, 2, true, UNAL>(a, stream);
 }
 
@@ -814,19 +858,18 @@ void embed_stream(const LinearArgs& a, hipStream_t stream)
     }
 }
 
+// The streamed form where it fits, at any number of tokens (1 to 4096 tokens of
+// 768 to 128 channels 6.7 to 7.1 us; direct form 8.7 to 9.2, tiles 12.7 to 14.1).
+// Elsewhere few tokens take the direct form up to 256 channels (4096 tokens of
+// 2048 to 128 channels 18.3 us, tiles 27.8) and tiles beyond, where one workgroup
+// reads too many weights (32 tokens of 1024 to 1024 channels 25.7 us, direct 40.4).
 void embed_once(const LinearArgs& a, hipStream_t stream)
 {
-    if (a.T > 4096 && stream_ok(a)) return embed_stream(a, stream);
-    if (a.T <= 4096) {
-        if (a.N <= 128) run_few<1, 1, 8, 2, true>(a, stream);
-        else if (a.N <= 256) run_few<1, 1, 16, 1, true>(a, stream);
-        else if (a.N <= 512) run_few<1, 2, 16, 1, true>(a, stream);
-        else run_few<1, 4, 16, 1, true>(a, stream);
-    } else if (a.K % 16 == 0) {
-        embed_tiles<false>(a, stream);
-    } else {
-        embed_tiles<true>(a, stream);
-    }
+    if (stream_ok(a)) return embed_stream(a, stream);
+    if (a.T <= 4096 && a.N <= 128) return run_few<1, 1, 8, 2, true>(a, stream);
+    if (a.T <= 4096 && a.N <= 256) return run_few<1, 1, 16, 1, true>(a, stream);
+    if (a.K % 16 == 0) embed_tiles<false>(a, stream);
+    else embed_tiles<true>(a, stream);
 }
 
 // One launch covers at most `step` rows, so that a grid's threads stay below

@@ -273,7 +273,7 @@ EMBED = [
     (40, 300, 200), (50, 513, 1024), (10, 1024, 2048), (18, 1023, 77), (4097, 128, 768),
     (4500, 48, 300), (5000, 96, 77), (4200, 200, 256), (6000, 256, 400), (4300, 300, 96),
     (4100, 512, 1040), (4099, 513, 64), (5001, 1024, 320), (4098, 770, 130), (4200, 5, 33),
-    (4120, 384, 72),
+    (4120, 384, 72), (70, 600, 1000), (33, 768, 4096), (300, 128, 4096), (4200, 128, 8192), (4300, 250, 2049),
     # many tokens, a projection that stays in registers: every depth and width class
     (5000, 96, 128), (4999, 128, 384), (9000, 40, 640), (4111, 128, 1024), (40000, 128, 768),
     (4500, 130, 256), (4100, 256, 512), (9001, 250, 896), (5003, 200, 768), (20000, 256, 1024),
