@@ -157,49 +157,11 @@ __device__ __forceinline__ void static_for(F&& f)
 
 __device__ __forceinline__ double xor_lane(double v, int m) { return __shfl_xor(v, m, 64); }
 
-// The largest magnitude and the sum of squares of the rows that a workgroup
-// holds: joins each token's pair over the lanes that share it (lane / COLS) and
-// over the WN waves that hold other channels, in a fixed order. red holds
-// 2 x WN rows of `stride`; slot is the token's place in a row. Every wave of the
-// workgroup calls it once between two other barriers; waves that hold no sums
-// pass wn < 0.
-template <int TT, int COLS, int WN>
-__device__ __forceinline__ void join_rows(double (&top)[TT], double (&ss)[TT], double* red, int stride,
-                                          const int (&slot)[TT], int wn)
-{
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int m = COLS; m < 64; m *= 2) {
-            top[t] = __builtin_fmax(top[t], xor_lane(top[t], m));
-            ss[t] += xor_lane(ss[t], m);
-        }
-    if constexpr (WN > 1) {
-        if (wn >= 0 && lane_id() < COLS) {
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                red[wn * stride + slot[t]] = top[t];
-                red[(WN + wn) * stride + slot[t]] = ss[t];
-            }
-        }
-        block_barrier();
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            top[t] = red[slot[t]];
-            ss[t] = red[WN * stride + slot[t]];
-#pragma unroll
-            for (int w = 1; w < WN; ++w) {
-                top[t] = __builtin_fmax(top[t], red[w * stride + slot[t]]);
-                ss[t] += red[(WN + w) * stride + slot[t]];
-            }
-        }
-    }
-}
-
-// Normalises the rows that a workgroup holds and writes them. For each of TT
-// tokens a lane holds NB runs of R consecutive channels: get(tt, b, i) is the
-// int32 sum of channel chan(b) + i. ws and bs (LDS) hold the scales and biases
-// of the workgroup's channels, 0 past the last one.
+// The sums of one call, normalised and written in two halves with a barrier
+// between them. For each of TT tokens a lane holds NB runs of R consecutive
+// channels: sum(tt, b, i) is the int32 sum of channel chan(b) + i.
+// ws and bs (LDS) hold the scales and biases of the workgroup's channels, 0 past
+// the last one.
 //
 // With s the largest magnitude of the row, its values over the norm are
 // (y / s) / ||y / s||, whose factors neither overflow nor vanish; the sum of
@@ -207,75 +169,155 @@ __device__ __forceinline__ void join_rows(double (&top)[TT], double (&ss)[TT], d
 // the nearest integers to 127 y / s: y and s are float64 there, so that a value
 // next to the middle between two codes is not moved across it, and adding
 // 1.5 * 2^52 in the product's fma leaves the integer in the low bits.
-template <int TT, int NB, int R, int COLS, int WN, typename GET, typename CHAN>
-__device__ __forceinline__ void embed_rows(const LinearArgs& a, GET get, CHAN chan, const float* ws, const float* bs,
+template <bool CODES, int TT, int NB, int R, int COLS, int WN>
+struct Rows {
+    // a lane's values stay in registers between the halves if they are few
+    // (otherwise they are computed again: 64 to 128 of them would spill)
+    static constexpr bool kKeep = TT * NB * R <= 16;
+    double top[TT], ss[TT];
+    double y64[CODES && kKeep ? 16 : 1];
+    float y32[!CODES && kKeep ? 16 : 1];
+
+    // Statistics of the lane's own channels.
+    template <typename SUM, typename CHAN>
+    __device__ __forceinline__ void first(SUM sum, CHAN chan, const float* ws, const float* bs, const float (&as)[TT],
+                                          const bool (&live)[TT])
+    {
+        static_for<0, TT>([&](auto tt) {
+            double m = 0.0, s2 = 0.0;
+            float mf = 0.0f;
+            static_for<0, NB>([&](auto b) {
+                static_for<0, R>([&](auto i) {
+                    const float w = ws[chan(b) + i], c = bs[chan(b) + i];
+                    if constexpr (CODES) {
+                        const double y = scaled64(sum(tt, b, i), (double)as[tt], w, c);
+                        m = __builtin_fmax(m, __builtin_fabs(y));
+                        s2 = __builtin_fma(y, y, s2);
+                        if constexpr (kKeep) y64[b * R + i] = y;
+                    } else {
+                        const float y = scaled(sum(tt, b, i), as[tt], w, c);
+                        mf = __builtin_fmaxf(mf, __builtin_fabsf(y));
+                        s2 = __builtin_fma((double)y, (double)y, s2);
+                        if constexpr (kKeep) y32[b * R + i] = y;
+                    }
+                });
+                run_ends();
+            });
+            top[tt] = !live[tt] ? 0.0 : CODES ? m : (double)mf;
+            ss[tt] = s2;
+        });
+    }
+
+    // The sum again, as a value the compiler cannot tie to the first half's, and
+    // the end of a run, over which it moves nothing: conversions kept or scales
+    // loaded ahead for all runs would spill.
+    static __device__ __forceinline__ int again(int s)
+    {
+        asm("" : "+v"(s));
+        return s;
+    }
+    static __device__ __forceinline__ void run_ends()
+    {
+        if constexpr (!kKeep) __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // Joins each token's statistics over the lanes that share it (lane / COLS), in a
+    // fixed order, and leaves them for the WN waves that hold other channels in
+    // red: 2 x WN rows of `stride`, slot the token's place. Waves that hold no
+    // sums pass wn < 0.
+    __device__ __forceinline__ void put(double* red, int stride, const int (&slot)[TT], int wn)
+    {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int m = COLS; m < 64; m *= 2) {
+                top[t] = __builtin_fmax(top[t], xor_lane(top[t], m));
+                ss[t] += xor_lane(ss[t], m);
+            }
+        if (WN > 1 && wn >= 0 && lane_id() < COLS) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                red[wn * stride + slot[t]] = top[t];
+                red[(WN + wn) * stride + slot[t]] = ss[t];
+            }
+        }
+    }
+
+    // After a barrier: the rows' statistics, and the outputs.
+    template <typename SUM, typename CHAN>
+    __device__ __forceinline__ void second(const LinearArgs& a, SUM sum, CHAN chan, const float* ws, const float* bs,
+                                           const int64_t (&t)[TT], const float (&as)[TT], const bool (&live)[TT],
+                                           const double* red, int stride, const int (&slot)[TT], int wn)
+    {
+        if constexpr (WN > 1) {
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                top[tt] = red[slot[tt]];
+                ss[tt] = red[WN * stride + slot[tt]];
+#pragma unroll
+                for (int w = 1; w < WN; ++w) {
+                    top[tt] = __builtin_fmax(top[tt], red[w * stride + slot[tt]]);
+                    ss[tt] += red[(WN + w) * stride + slot[tt]];
+                }
+            }
+        }
+        // zero rows are multiplied by 0: their values are finite
+        static_for<0, TT>([&](auto tt) {
+            const bool in = t[tt] < a.T;
+            if constexpr (!CODES) {
+                const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
+                const float inv = zero ? 0.0f : 1.0f / (float)top[tt];
+                // the rest of the norm is between 1 and the square root of N
+                const float r = zero ? 0.0f : __builtin_amdgcn_rsqf((float)(ss[tt] * (double)inv * (double)inv));
+                static_for<0, NB>([&](auto b) {
+                    float y[R];
+                    static_for<0, R>([&](auto i) {
+                        if constexpr (kKeep) y[i] = y32[b * R + i] * inv * r;
+                        else y[i] = scaled(again(sum(tt, b, i)), as[tt], ws[chan(b) + i], bs[chan(b) + i]) * inv * r;
+                    });
+                    if (in) store_run<R>(a.Y, a.out, t[tt], chan(b), a.N, y);
+                    run_ends();
+                });
+            } else {
+                const bool zero = !(top[tt] >= (double)kTiny);
+                const double inv = zero ? 0.0 : 127.0 / top[tt];
+                static_for<0, NB>([&](auto b) {
+                    uint32_t q[R];
+                    static_for<0, R>([&](auto i) {
+                        double y;
+                        if constexpr (kKeep) y = y64[b * R + i];
+                        else y = scaled64(again(sum(tt, b, i)), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
+                        q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(y, inv, 0x1.8p52));
+                    });
+                    if (in) store_codes<R>(a.Y, t[tt], chan(b), a.N, q);
+                    run_ends();
+                });
+                // codes * scale is y / ||y||, so scale = 1 / ||127 y / s||
+                if (in && wn == 0 && lane_id() < COLS)
+                    a.y_scale[t[tt]] = zero ? 1.0f : __builtin_amdgcn_rsqf((float)(ss[tt] * inv * inv));
+            }
+        });
+    }
+};
+
+template <int TT, int NB, int R, int COLS, int WN, typename SUM, typename CHAN>
+__device__ __forceinline__ void embed_rows(const LinearArgs& a, SUM sum, CHAN chan, const float* ws, const float* bs,
                                            const int64_t (&t)[TT], const float (&as)[TT], const bool (&live)[TT],
                                            const int (&slot)[TT], int wn, double* red, int stride)
 {
-    double top[TT], ss[TT];
-    static_for<0, TT>([&](auto tt) {
-        double s2 = 0.0;
-        if (a.out != kI8) {
-            float m = 0.0f;
-            static_for<0, NB>([&](auto b) {
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float y = scaled(get(tt, b, i), as[tt], ws[chan(b) + i], bs[chan(b) + i]);
-                    m = __builtin_fmaxf(m, __builtin_fabsf(y));
-                    s2 = __builtin_fma((double)y, (double)y, s2);
-                }
-            });
-            top[tt] = live[tt] ? (double)m : 0.0;
-        } else {
-            double m = 0.0;
-            static_for<0, NB>([&](auto b) {
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const double y = scaled64(get(tt, b, i), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
-                    m = __builtin_fmax(m, __builtin_fabs(y));
-                    s2 = __builtin_fma(y, y, s2);
-                }
-            });
-            top[tt] = live[tt] ? m : 0.0;
-        }
-        ss[tt] = s2;
-    });
-    join_rows<TT, COLS, WN>(top, ss, red, stride, slot, wn);
-    static_for<0, TT>([&](auto tt) {
-        const bool in = t[tt] < a.T;
-        if (a.out != kI8) {
-            const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
-            const float inv = 1.0f / (float)top[tt];
-            const float r = __builtin_amdgcn_rsqf((float)(ss[tt] * (double)inv * (double)inv));  // 1 .. N inside
-            if (in) {
-                static_for<0, NB>([&](auto b) {
-                    float y[R];
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-                        y[i] = zero ? 0.0f
-                                    : scaled(get(tt, b, i), as[tt], ws[chan(b) + i], bs[chan(b) + i]) * inv * r;
-                    store_run<R>(a.Y, a.out, t[tt], chan(b), a.N, y);
-                });
-            }
-        } else {
-            const bool zero = !(top[tt] >= (double)kTiny);
-            const double inv = zero ? 0.0 : 127.0 / top[tt];
-            if (in) {
-                static_for<0, NB>([&](auto b) {
-                    uint32_t q[R];
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const double y = scaled64(get(tt, b, i), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
-                        q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(zero ? 0.0 : y, inv, 0x1.8p52));
-                    }
-                    store_codes<R>(a.Y, t[tt], chan(b), a.N, q);
-                });
-                // codes * scale is y / ||y||, so scale = 1 / ||127 y / s||
-                if (wn == 0 && lane_id() < COLS)
-                    a.y_scale[t[tt]] = zero ? 1.0f : __builtin_amdgcn_rsqf((float)(ss[tt] * inv * inv));
-            }
-        }
-    });
+    auto go = [&](auto& rows) {
+        rows.first(sum, chan, ws, bs, as, live);
+        rows.put(red, stride, slot, wn);
+        if (WN > 1) block_barrier();
+        rows.second(a, sum, chan, ws, bs, t, as, live, red, stride, slot, wn);
+    };
+    if (a.out == kI8) {
+        Rows<true, TT, NB, R, COLS, WN> rows;
+        go(rows);
+    } else {
+        Rows<false, TT, NB, R, COLS, WN> rows;
+        go(rows);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -537,7 +579,7 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
             as[j] = live[j] ? a.a_scale[t[j]] : 0.0f;
         }
         embed_rows<C::TT, C::NT, 16, 32, WN>(
-            a, [&](auto j, auto b, int i) { return acc[b][j][i]; },
+            a, [&](auto j, auto b, auto i) { return acc[b][j][(int)i]; },
             [&](int b) { return (wn * C::NT + b) * 32 + half * 16; }, ws, bs, t, as, live, slot, wn, red, BT);
     } else {
         store_tile<C::NT, C::TT>(a, acc, ws, bs, t0, n0, a_row, wn, wave, ring);
@@ -553,7 +595,7 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
 // whole run, and the hidden states stream through an LDS ring of ST stages, 32
 // whole rows each, one contiguous piece of memory. Nothing but the states is
 // read again and again, each byte once.
-template <int KS, int NWV, int ST>
+template <int KS, int NWV, int ST, bool CODES>
 __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
 {
     constexpr int kScales = KS * 1024, kMask = kScales + 256, kStage = kMask + 256;
@@ -561,7 +603,7 @@ __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
     constexpr int kLoads = PW + 2;            // and the tokens' scales and mask
     __shared__ __align__(1024) uint8_t ring[ST * kStage];
     __shared__ __align__(16) float ws[NWV * 32], bs[NWV * 32];
-    __shared__ double red[2 * NWV * 32];
+    __shared__ double red[2 * 2 * NWV * 32];
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id(), l = lane & 31, half = lane >> 5;
     const int K = a.K;
 
@@ -621,13 +663,26 @@ __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
         if (s < count) issue(s);
+    // One barrier per tile: it hands over the tile that landed and, with it, the
+    // statistics of the tile before, which is normalised and written beside the
+    // next one's MFMAs.
+    Rows<CODES, 1, 1, 16, 32, NWV> rows{};
+    int64_t t[1] = {a.T};  // no tile before the first
+    float as[1];
+    bool live[1] = {false};
+    const int slot[1] = {l};
+    i32x16 acc;
+    auto sum = [&](auto, auto, auto r) { return acc[(int)r]; };
+    auto chan = [&](int) { return wave * 32 + half * 16; };
+    auto finish = [&](int i) {
+        rows.second(a, sum, chan, ws, bs, t, as, live, red + (i & 1) * (2 * NWV * 32), 32, slot, wave);
+    };
     for (int i = 0; i < count; ++i) {
         if (i + ST - 2 < count) wait_vmcnt<(ST - 2) * kLoads>();
         else wait_vmcnt<0>();
         block_barrier();  // all waves' loads of stage i landed; stage i - 1 is read
         if (i + ST - 1 < count) issue(i + ST - 1);
         const uint8_t* st = ring + (i % ST) * kStage;
-        i32x16 acc;
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[r] = 0;
         // where K < KS * 32, the last fragments of w are zeros and the bytes they
@@ -635,15 +690,15 @@ __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
             acc = mfma32<kI8>(w[s], *(const i32x4*)(st + off[s & 7] + (s >> 3) * 256), acc);
-        const int64_t t0 = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * 32;
-        const int64_t t[1] = {t0 + l};
-        const bool live[1] = {t[0] < a.T && (!a.mask || st[kMask + mask_at + l])};
-        const float as[1] = {live[0] ? *(const float*)(st + kScales + l * 4) : 0.0f};
-        const int slot[1] = {l};
-        embed_rows<1, 1, 16, 32, NWV>(
-            a, [&](auto, auto, int r) { return acc[r]; }, [&](int) { return wave * 32 + half * 16; }, ws, bs, t, as,
-            live, slot, wave, red, 32);
+        finish(i + 1);
+        t[0] = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * 32 + l;
+        live[0] = t[0] < a.T && (!a.mask || st[kMask + mask_at + l]);
+        as[0] = live[0] ? *(const float*)(st + kScales + l * 4) : 0.0f;
+        rows.first(sum, chan, ws, bs, as, live);
+        rows.put(red + (i & 1) * (2 * NWV * 32), 32, slot, wave);
     }
+    block_barrier();
+    finish(count - 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -747,7 +802,7 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
             if (!live[j]) as[j] = 0.0f;
         }
         embed_rows<TT, NPW, 4, 16, NW>(
-            a, [&](auto j, auto b, int i) { return acc[b][j][i]; },
+            a, [&](auto j, auto b, auto i) { return acc[b][j][(int)i]; },
             [&](int b) { return (nw * NPW + b) * 16 + quarter * 4; }, ws, bs, t, as, live, slot, kw == 0 ? nw : -1, red,
             TT * 16);
     } else {
@@ -837,8 +892,9 @@ void run_stream(LinearArgs a, hipStream_t stream)
 {
     a.tiles_t = (int32_t)tiles(a.T, 32);
     const int64_t most = (int64_t)device_cu_count() * (8 / NWV);  // 8 waves on each CU
-    hipLaunchKernelGGL((stream_kernel<KS, NWV, ST>), dim3((unsigned)(a.tiles_t < most ? a.tiles_t : most)),
-                       dim3(NWV * 64), 0, stream, a);
+    const dim3 grid((unsigned)(a.tiles_t < most ? a.tiles_t : most)), block(NWV * 64);
+    if (a.out == kI8) hipLaunchKernelGGL((stream_kernel<KS, NWV, ST, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((stream_kernel<KS, NWV, ST, false>), grid, block, 0, stream, a);
 }
 
 // The ring's stages: 72 KB a workgroup where two share a CU's LDS, 150 KB for one.
