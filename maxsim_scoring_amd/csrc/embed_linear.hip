@@ -281,13 +281,15 @@ struct Rows {
             } else {
                 const bool zero = !(top[tt] >= (double)kTiny);
                 const double inv = zero ? 0.0 : 127.0 / top[tt];
+                double magic = 0x1.8p52;
+                asm("" : "+v"(magic));  // a register: as a constant it is copied for every fma
                 static_for<0, NB>([&](auto b) {
                     uint32_t q[R];
                     static_for<0, R>([&](auto i) {
                         double y;
                         if constexpr (kKeep) y = y64[b * R + i];
                         else y = scaled64(again(sum(tt, b, i)), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
-                        q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(y, inv, 0x1.8p52));
+                        q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(y, inv, magic));
                     });
                     if (in) store_codes<R>(a.Y, t[tt], chan(b), a.N, q);
                     run_ends();
@@ -625,13 +627,12 @@ __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
     const bool even = (K & 255) == 0;
     auto f = [&](int r) { return even ? r & 15 : (r >> 1) & 7; };
     const int cpr = K / 16, loads = K / 32;
-    int row_of[PW], at_of[PW];
+    auto load_of = [&](int j) { return wave * PW + j < loads ? wave * PW + j : loads - 1; };  // a spare load
+    uint32_t voff[PW];                                                                        // repeats the last
 #pragma unroll
     for (int j = 0; j < PW; ++j) {
-        const int load = wave * PW + j < loads ? wave * PW + j : loads - 1;  // a spare load repeats the last
-        const int p = load * 64 + lane;
-        row_of[j] = p / cpr;
-        at_of[j] = ((p % cpr) ^ f(row_of[j])) * 16;
+        const int p = load_of(j) * 64 + lane, r = p / cpr;
+        voff[j] = (uint32_t)(r * K + ((p % cpr) ^ f(r)) * 16);
     }
     const uint32_t ring0 = lds_addr(ring);
     const int count = (a.tiles_t - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;  // tiles of this workgroup
@@ -642,9 +643,12 @@ __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
         const void* src = uniform_ptr(a.A + t0 * K);
 #pragma unroll
         for (int j = 0; j < PW; ++j) {
-            const int load = wave * PW + j < loads ? wave * PW + j : loads - 1;
-            dma_lds16_nt(src, (uint32_t)((row_of[j] < last ? row_of[j] : last) * K + at_of[j]),
-                         (uint32_t)uniform((int)(to + load * 1024)));
+            uint32_t v = voff[j];
+            if (last < 31) {  // rows past the end repeat the last one
+                const int r = (load_of(j) * 64 + lane) / cpr;
+                v -= (uint32_t)((r > last ? r - last : 0) * K);
+            }
+            dma_lds16_nt(src, v, (uint32_t)uniform((int)(to + load_of(j) * 1024)));
         }
         // every wave brings the 32 scales and mask bytes, so that all count alike
         dma_lds4(uniform_ptr(a.a_scale + t0), (uint32_t)(lane < last ? lane : last) * 4,
