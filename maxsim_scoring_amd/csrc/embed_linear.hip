@@ -16,24 +16,15 @@
 // memory to registers, waves split k, and LDS joins their sums.
 #include <type_traits>
 
-#include "common.hpp"
+#include "embed_common.hpp"
 #include "kernels.hpp"
 
 namespace maxsim {
 
 namespace {
 
-constexpr float kTiny = 0x1p-110f;  // rows below this count as zeros
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
-
-__device__ __forceinline__ uint32_t half_bits(int out, float v)
-{
-    return out == kBF16 ? (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v)
-                        : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v);
-}
 
 // 16 bytes of a row of K bytes from byte k on (k a multiple of 16); bytes past
 // the row's end are 0. UNAL: the row may start at any byte address. Only bytes
@@ -268,7 +259,7 @@ struct Rows {
                 const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
                 const float inv = zero ? 0.0f : 1.0f / (float)top[tt];
                 // the rest of the norm is between 1 and the square root of N
-                const float r = zero ? 0.0f : __builtin_amdgcn_rsqf((float)(ss[tt] * (double)inv * (double)inv));
+                const float r = zero ? 0.0f : rsqrt_f((float)(ss[tt] * (double)inv * (double)inv));
                 static_for<0, NB>([&](auto b) {
                     float y[R];
                     static_for<0, R>([&](auto i) {
@@ -296,7 +287,7 @@ struct Rows {
                 });
                 // codes * scale is y / ||y||, so scale = 1 / ||127 y / s||
                 if (in && wn == 0 && lane_id() < COLS)
-                    a.y_scale[t[tt]] = zero ? 1.0f : __builtin_amdgcn_rsqf((float)(ss[tt] * inv * inv));
+                    a.y_scale[t[tt]] = zero ? 1.0f : rsqrt_f((float)(ss[tt] * inv * inv));
             }
         });
     }

@@ -143,6 +143,56 @@ def test_rows_beyond_32_bit_offsets(ms):
         assert np.array_equal(got, np.where(gone, 0.0, 2 * src)), first  # twice a bf16 is exact
 
 
+def test_more_rows_than_a_grid(ms):
+    """Grids are capped and launches split; rows on both sides of every seam."""
+    T = (1 << 28) + 77  # 2^22 workgroups of 64 rows
+    x = torch.ones(T, 1, dtype=torch.bfloat16, device=DEV)
+    at = torch.tensor([0, (1 << 28) - 1, 1 << 28, T - 1], device=DEV)
+    x[at, 0] = torch.tensor([-2.0, 0.0, 4.0, -8.0], device=DEV).bfloat16()
+    codes, scale = ms.maxsim_quantize_tok(x)
+    assert codes[at, 0].tolist() == [-127, 0, 127, -127]
+    assert torch.equal(scale[at], (torch.tensor([2.0, 127.0, 4.0, 8.0], device=DEV) / 127))
+    assert bool((codes == 127).sum() == T - 3)
+    del codes, scale
+    y, rn = ms.maxsim_normalize_fwd(x)
+    assert y[at, 0].tolist() == [-1, 0, 1, -1] and rn[at].tolist() == [0.5, 0, 0.25, 0.125]
+    dx = ms.maxsim_normalize_bwd(x, rn, torch.ones(T, 1, device=DEV))
+    assert not dx.any()  # a row of one value has no direction to change
+    del x, y, rn, dx
+    T, K, N = (1 << 26) + 333, 16, 5
+    g = _gen(6)
+    a = torch.empty(T, K, dtype=torch.int8, device=DEV).random_(-127, 128, generator=g)
+    s = torch.rand(T, generator=g, device=DEV) + 0.5
+    m = torch.ones(T, dtype=torch.uint8, device=DEV)
+    _, _, w, ws, b = _operands(1, N, K, 8)
+    at = torch.tensor([0, (1 << 24) - 1, 1 << 24, (1 << 26) - 1, 1 << 26, T - 1], device=DEV)
+    m[at[2]] = 0
+    y64, p64 = ref.linear(a[at].cpu().numpy(), f64(s[at]), w.cpu().numpy(), f64(ws), f64(b))
+    y = ms.maxsim_linear_i8(a, s, w, ws, b)
+    _within("product", y[at], y64, ref.linear_bound(y64, p64, torch.bfloat16))
+    del y
+    e, scale = ms.maxsim_embed_i8(a, s, w, ws, b, m)
+    codes, want, gap = ref.quantize(y64, f64(m[at]), normalize=True)
+    assert gap.min() > 1e-6 and np.array_equal(e[at].cpu().numpy(), codes)
+    _within("scale", scale[at], want, want * 100 * ref.U)
+
+
+def test_dropout_past_a_grid(ms):
+    """2^22 workgroups of 2,048 elements and some more."""
+    n = (1 << 33) + 1003
+    x = torch.empty(n, dtype=torch.bfloat16, device=DEV)
+    windows = (0, (1 << 33) - 64, 1 << 33, n // 8 * 8 - 64)
+    for i, first in enumerate(windows):
+        x[first:first + 64] = torch.arange(1, 65, device=DEV) + i
+    x[n - 3:] = 3
+    y = ms.maxsim_dropout_fwd(x, 0.5, 21, 4)
+    for i, first in enumerate(windows):
+        gone = ref.dropped(64, 0.5, 21, 4, first)
+        assert np.array_equal(f64(y[first:first + 64]), np.where(gone, 0.0, 2.0 * (np.arange(1, 65) + i))), first
+    gone = ref.dropped(n % 8, 0.5, 21, 4, n // 8 * 8)
+    assert np.array_equal(f64(y[n - 3:]), np.where(gone[-3:], 0.0, 6.0))
+
+
 # ------------------------------------------------------------ normalisation
 
 @by_type
@@ -424,6 +474,33 @@ def test_side_streams(ms):
     torch.cuda.synchronize()
     for (e, s), (e0, s0) in zip(got, want):
         assert torch.equal(e, e0) and torch.equal(s, s0)
+
+
+def test_captured_serving_run(ms):
+    """Two captured graphs of the same operators, replayed in turn and at once
+    on streams of their own, against the eager results."""
+    w, ws = _operands(1, 128, 384, 5)[2:4]
+    xs = [_rows(500 + 700 * i, 384, torch.bfloat16, 70 + i) for i in range(2)]
+    graphs, outs = [], []
+    for x in xs:
+        ms.embed_tokens_i8(x, w, ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ms.embed_tokens_i8(x, w, ws))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in xs]
+    for i in range(4):
+        for x in xs:
+            x.mul_(-1.5)
+        want = [ms.embed_tokens_i8(x, w, ws) for x in xs]
+        for g, s in zip(graphs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (e, s), (e0, s0) in zip(outs, want):
+            assert torch.equal(e, e0) and torch.equal(s, s0)
 
 
 def test_captured_training_step(ms):
