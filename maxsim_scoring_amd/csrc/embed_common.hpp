@@ -26,4 +26,15 @@ __device__ __forceinline__ uint32_t half_bits(int out, float v)
                         : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
+// Two values rounded to the 16-bit type `out`, the first in the low half.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+template <int OUT>
+__device__ __forceinline__ uint32_t half_pair(float a, float b)
+{
+    if constexpr (OUT == kBF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
+}
+
 }  // namespace maxsim

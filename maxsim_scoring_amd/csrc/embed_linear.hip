@@ -92,10 +92,10 @@ __device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, in
     uint32_t w[R / 2];
     if (out == kBF16) {
 #pragma unroll
-        for (int i = 0; i < R / 2; ++i) w[i] = half_bits(kBF16, y[2 * i]) | half_bits(kBF16, y[2 * i + 1]) << 16;
+        for (int i = 0; i < R / 2; ++i) w[i] = half_pair<kBF16>(y[2 * i], y[2 * i + 1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < R / 2; ++i) w[i] = half_bits(kF16, y[2 * i]) | half_bits(kF16, y[2 * i + 1]) << 16;
+        for (int i = 0; i < R / 2; ++i) w[i] = half_pair<kF16>(y[2 * i], y[2 * i + 1]);
     }
     if (R == 16 && (N & 7) == 0) {
 #pragma unroll
@@ -414,19 +414,36 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, const i32x16 (&a
         }
         return;
     }
+    // 16-bit outputs whose channels all exist need no test per piece
+    const bool whole = a.out != kF32 && (a.N & 7) == 0 && n0 + (wn + 1) * NT * 32 <= a.N;
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
         const int64_t t = t0 + a_row + j * 32 + (lane & 31);
         if (t >= a.T) continue;
         const float as = a.a_scale[t];
+        uint16_t* row = (uint16_t*)a.Y + t * a.N + n0;
+        auto runs = [&](auto put) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int n = (wn * NT + i) * 32 + half * 16;
-            float y[16];
+            for (int i = 0; i < NT; ++i) {
+                const int n = (wn * NT + i) * 32 + half * 16;
+                float y[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = scaled(acc[i][j][e], as, ws[n + e], bs[n + e]);
-            store_run<16>(a.Y, a.out, t, n0 + n, a.N, y);
-        }
+                for (int e = 0; e < 16; ++e) y[e] = scaled(acc[i][j][e], as, ws[n + e], bs[n + e]);
+                put(n, y);
+            }
+        };
+        auto pack = [&](auto out) {
+            runs([&](int n, const float (&y)[16]) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = half_pair<out>(y[2 * i], y[2 * i + 1]);
+                ((u32x4*)(row + n))[0] = u32x4{w[0], w[1], w[2], w[3]};
+                ((u32x4*)(row + n))[1] = u32x4{w[4], w[5], w[6], w[7]};
+            });
+        };
+        if (whole && a.out == kBF16) pack(std::integral_constant<int, kBF16>{});
+        else if (whole) pack(std::integral_constant<int, kF16>{});
+        else runs([&](int n, const float (&y)[16]) { store_run<16>(a.Y, a.out, t, n0 + n, a.N, y); });
     }
 }
 

@@ -71,10 +71,10 @@ __device__ __forceinline__ void store(void* Y, int out, int64_t at, const float 
         uint32_t w[C / 2];
         if (out == kBF16) {
 #pragma unroll
-            for (int i = 0; i < C / 2; ++i) w[i] = half_bits(kBF16, y[2 * i]) | half_bits(kBF16, y[2 * i + 1]) << 16;
+            for (int i = 0; i < C / 2; ++i) w[i] = half_pair<kBF16>(y[2 * i], y[2 * i + 1]);
         } else {
 #pragma unroll
-            for (int i = 0; i < C / 2; ++i) w[i] = half_bits(kF16, y[2 * i]) | half_bits(kF16, y[2 * i + 1]) << 16;
+            for (int i = 0; i < C / 2; ++i) w[i] = half_pair<kF16>(y[2 * i], y[2 * i + 1]);
         }
         if constexpr (C == 8) *(u32x4*)p = u32x4{w[0], w[1], w[2], w[3]};
         else *(u32x2*)p = u32x2{w[0], w[1]};
