@@ -30,7 +30,6 @@ namespace maxsim {
 
 namespace {
 
-
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
 
 // 16 bytes of a row of K bytes from byte k on (k a multiple of 16); bytes past

@@ -302,6 +302,21 @@ def test_linear_extremes(ms, T):
     assert torch.equal(y, want)  # float32 of the whole numbers
 
 
+@pytest.mark.parametrize("T", [2, 40])
+def test_linear_most_channels(ms, T):
+    """2^26 output channels: 1 GB of weights, 5 GB of outputs, launches in parts."""
+    N, K = 1 << 26, 16
+    g = _gen(T)
+    a = torch.randint(-128, 128, (T, K), generator=g, device=DEV, dtype=torch.int8)
+    w = torch.empty(N, K, dtype=torch.int8, device=DEV).random_(-127, 128, generator=g)
+    s = torch.rand(T, generator=g, device=DEV) + 0.5
+    ws = torch.rand(N, generator=g, device=DEV) + 0.5
+    y = ms.maxsim_linear_i8(a, s, w, ws)
+    at = torch.tensor([0, 1, (1 << 25) - 1, 1 << 25, N - 257, N - 1], device=DEV)
+    y64, p64 = ref.linear(a.cpu().numpy(), f64(s), w[at].cpu().numpy(), f64(ws[at]))
+    _within("product", y[:, at], y64, ref.linear_bound(y64, p64, torch.bfloat16))
+
+
 def test_linear_rows_beyond_32_bit_offsets(ms):
     T, K, N = 4_300_000, 1024, 24
     g = _gen(4)
@@ -427,6 +442,15 @@ def test_no_rows(ms):
         assert ms.maxsim_linear_i8(c, s, w, ws).shape == lead + (8,)
         assert ms.maxsim_embed_i8(c, s, w, ws)[1].shape == lead
         assert ms.maxsim_dropout_fwd(x, 0.5, 1).shape == x.shape
+
+
+def test_one_row_without_leading_dimensions(ms):
+    x = _rows(1, 200, torch.float32, 3).view(200)
+    c, s = ms.maxsim_quantize_tok(x)
+    assert c.shape == (200,) and s.shape == () and (c.abs() <= 127).all()
+    y, r = ms.maxsim_normalize_fwd(x)
+    assert y.shape == (200,) and abs(float(y.norm()) - 1) < 1e-5
+    assert ms.maxsim_normalize_bwd(x, r, y).abs().max() < 1e-5  # along the row itself nothing changes
 
 
 def test_leading_dimensions_and_refusals(ms):
