@@ -553,46 +553,42 @@ def _row_type(name: str, dtype) -> int:
     return _ROW_TYPES[dtype]
 
 
-class _On:
-    """The device and stream of one call: the device of its first tensor, and
-    that device's current stream unless one is given. Entered, both are
-    current, so the call launches there and the outputs it allocates belong to
-    that stream."""
-
-    __slots__ = ("_ctx", "handle")
-
-    def __init__(self, stream, tensors):
-        dev = tensors[0][1].device
-        for name, t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a GPU tensor")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-            if t.device != dev:
-                raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        self._ctx = None
-        if stream is None:
-            # the raw handle: building a Stream object takes longer than the checks
-            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
-            if dev.index != torch._C._cuda_getDevice():
-                self._ctx = torch.cuda.device(dev)
+def _place(names: str, *tensors) -> int:
+    """The device index of one call's tensors (None for those left out): all on
+    one GPU, all contiguous."""
+    index = tensors[0].get_device()
+    if index >= 0:
+        for t in tensors:
+            if t is not None and (t.get_device() != index or not t.is_contiguous()):
+                break
         else:
-            if stream.device != dev:
-                raise ValueError(f"stream must be one of {dev}, got {stream.device}")
-            self.handle = stream.cuda_stream
-            self._ctx = torch.cuda.stream(stream)
+            return index
+    for name, t in zip(names.split(), tensors):
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on GPU {index}, got {t.device}")
+    raise AssertionError("unreachable")
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self.handle
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        return False
+def _elsewhere(stream, index: int):
+    """None where a call can launch at once: on its tensors' device, which is the
+    current one, and that device's current stream. Otherwise the context in
+    which it can, so that the outputs it allocates belong to that stream too."""
+    if stream is None:
+        return None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream must be one of GPU {index}, got {stream.device}")
+    return torch.cuda.stream(stream)
+
+
+# the current stream's handle: building a Stream object takes longer than the
+# call's checks
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -605,10 +601,12 @@ def _has(name: str, t: Optional[torch.Tensor], dtype, shape) -> None:
 
 
 def _rows(name: str, t: torch.Tensor):
-    """(leading shape, rows, width) of a tensor of rows."""
-    if t.dim() < 1:
+    """(shape, leading shape, rows, width) of a tensor of rows."""
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} must have rows in its last dimension")
-    return t.shape[:-1], math.prod(t.shape[:-1]), t.shape[-1]
+    lead, d = shape[:-1], shape[-1]
+    return shape, lead, t.numel() // d if d else math.prod(lead), d
 
 
 def maxsim_quantize_tok(X: torch.Tensor, mask: Optional[torch.Tensor] = None,
@@ -619,23 +617,27 @@ def maxsim_quantize_tok(X: torch.Tensor, mask: Optional[torch.Tensor] = None,
     ``normalize`` X over its row norms. mask uint8 [...]: masked rows (and rows
     of zeros) get codes 0, scale 1. Returns (codes int8 [..., d], scale float32 [...])."""
     code = _row_type("X", X.dtype)
-    lead, T, d = _rows("X", X)
+    shape, lead, T, d = _rows("X", X)
     _has("mask", mask, torch.uint8, lead)
-    _has("codes", codes, torch.int8, X.shape)
+    _has("codes", codes, torch.int8, shape)
     _has("scale", scale, torch.float32, lead)
-    with _On(stream, (("X", X), ("mask", mask), ("codes", codes), ("scale", scale))) as st:
-        if codes is None:
-            codes = torch.empty_like(X, dtype=torch.int8)
-        if scale is None:
-            scale = torch.empty(lead, dtype=torch.float32, device=X.device)
-        _check("maxsim_quantize_tok",
-               lib().maxsim_quantize_tok(code, X.data_ptr(), T, d, _at(mask), bool(normalize),
-                                         codes.data_ptr(), scale.data_ptr(), st))
+    index = _place("X mask codes scale", X, mask, codes, scale)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_quantize_tok(X, mask, normalize, codes, scale)
+    if codes is None:
+        codes = torch.empty_like(X, dtype=torch.int8)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=X.device)
+    _check("maxsim_quantize_tok",
+           lib().maxsim_quantize_tok(code, X.data_ptr(), T, d, _at(mask), bool(normalize),
+                                     codes.data_ptr(), scale.data_ptr(), _raw_stream(index)))
     return codes, scale
 
 
 def _linear_args(A, a_scale, W, w_scale, bias):
-    lead, T, K = _rows("A", A)
+    _, lead, T, K = _rows("A", A)
     if W.dim() != 2 or W.shape[1] != K:
         raise ValueError(f"W must be [N, {K}], got {list(W.shape)}")
     N = W.shape[0]
@@ -644,7 +646,7 @@ def _linear_args(A, a_scale, W, w_scale, bias):
     _has("a_scale", a_scale, torch.float32, lead)
     _has("w_scale", w_scale, torch.float32, (N,))
     _has("bias", bias, torch.float32, (N,))
-    return lead, T, K, N
+    return T, K, N, lead + (N,)
 
 
 def maxsim_linear_i8(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
@@ -653,17 +655,21 @@ def maxsim_linear_i8(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
     """8-bit product a_scale * w_scale * (A W^T) + bias. A int8 [..., K], a_scale
     float32 [...], W int8 [N, K], w_scale and bias float32 [N]. Returns Y [..., N]
     of ``out_dtype`` (fp16, bf16 or fp32)."""
-    lead, T, K, N = _linear_args(A, a_scale, W, w_scale, bias)
-    code = _row_type("out_dtype", out_dtype if Y is None else Y.dtype)
-    if Y is not None:
-        _has("Y", Y, Y.dtype, lead + (N,))
-    with _On(stream, (("A", A), ("a_scale", a_scale), ("W", W), ("w_scale", w_scale),
-                      ("bias", bias), ("Y", Y))) as st:
-        if Y is None:
-            Y = torch.empty(lead + (N,), dtype=out_dtype, device=A.device)
-        _check("maxsim_linear_i8",
-               lib().maxsim_linear_i8(code, A.data_ptr(), a_scale.data_ptr(), W.data_ptr(),
-                                      w_scale.data_ptr(), _at(bias), T, N, K, Y.data_ptr(), st))
+    T, K, N, shape = _linear_args(A, a_scale, W, w_scale, bias)
+    dt = out_dtype if Y is None else Y.dtype
+    code = _row_type("out_dtype", dt)
+    _has("Y", Y, dt, shape)
+    index = _place("A a_scale W w_scale bias Y", A, a_scale, W, w_scale, bias, Y)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_linear_i8(A, a_scale, W, w_scale, bias, dt, Y)
+    if Y is None:
+        Y = torch.empty(shape, dtype=dt, device=A.device)
+    _check("maxsim_linear_i8",
+           lib().maxsim_linear_i8(code, A.data_ptr(), a_scale.data_ptr(), W.data_ptr(),
+                                  w_scale.data_ptr(), _at(bias), T, N, K, Y.data_ptr(),
+                                  _raw_stream(index)))
     return Y
 
 
@@ -677,24 +683,29 @@ def maxsim_embed_i8(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
     maxsim_fwd_i8_tok, fp16, bf16 or fp32 the embeddings themselves. mask uint8
     [...]: masked rows give zeros (codes 0, scale 1). Returns (E [..., d],
     e_scale float32 [...] or None)."""
-    lead, T, K, d = _linear_args(A, a_scale, W, w_scale, bias)
+    T, K, d, shape = _linear_args(A, a_scale, W, w_scale, bias)
+    lead = shape[:-1]
     _has("mask", mask, torch.uint8, lead)
     dt = out_dtype if E is None else E.dtype
     code = MAXSIM_I8 if dt == torch.int8 else _row_type("out_dtype", dt)
     if code != MAXSIM_I8 and e_scale is not None:
         raise ValueError("e_scale is an output of int8 embeddings only")
-    _has("E", E, dt, lead + (d,))
+    _has("E", E, dt, shape)
     _has("e_scale", e_scale, torch.float32, lead)
-    with _On(stream, (("A", A), ("a_scale", a_scale), ("W", W), ("w_scale", w_scale),
-                      ("bias", bias), ("mask", mask), ("E", E), ("e_scale", e_scale))) as st:
-        if E is None:
-            E = torch.empty(lead + (d,), dtype=dt, device=A.device)
-        if e_scale is None and code == MAXSIM_I8:
-            e_scale = torch.empty(lead, dtype=torch.float32, device=A.device)
-        _check("maxsim_embed_i8",
-               lib().maxsim_embed_i8(code, A.data_ptr(), a_scale.data_ptr(), W.data_ptr(),
-                                     w_scale.data_ptr(), _at(bias), _at(mask), T, d, K,
-                                     E.data_ptr(), _at(e_scale), st))
+    index = _place("A a_scale W w_scale bias mask E e_scale", A, a_scale, W, w_scale, bias, mask, E,
+                   e_scale)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_embed_i8(A, a_scale, W, w_scale, bias, mask, dt, E, e_scale)
+    if E is None:
+        E = torch.empty(shape, dtype=dt, device=A.device)
+    if e_scale is None and code == MAXSIM_I8:
+        e_scale = torch.empty(lead, dtype=torch.float32, device=A.device)
+    _check("maxsim_embed_i8",
+           lib().maxsim_embed_i8(code, A.data_ptr(), a_scale.data_ptr(), W.data_ptr(),
+                                 w_scale.data_ptr(), _at(bias), _at(mask), T, d, K, E.data_ptr(),
+                                 _at(e_scale), _raw_stream(index)))
     return E, e_scale
 
 
@@ -718,18 +729,22 @@ def maxsim_normalize_fwd(X: torch.Tensor, mask: Optional[torch.Tensor] = None, o
     xt = _row_type("X", X.dtype)
     dt = Y.dtype if Y is not None else X.dtype if out_dtype is None else out_dtype
     yt = _row_type("out_dtype", dt)
-    lead, T, d = _rows("X", X)
+    shape, lead, T, d = _rows("X", X)
     _has("mask", mask, torch.uint8, lead)
-    _has("Y", Y, dt, X.shape)
+    _has("Y", Y, dt, shape)
     _has("rnorm", rnorm, torch.float32, lead)
-    with _On(stream, (("X", X), ("mask", mask), ("Y", Y), ("rnorm", rnorm))) as st:
-        if Y is None:
-            Y = torch.empty_like(X, dtype=dt)
-        if rnorm is None:
-            rnorm = torch.empty(lead, dtype=torch.float32, device=X.device)
-        _check("maxsim_normalize_fwd",
-               lib().maxsim_normalize_fwd(xt, X.data_ptr(), T, d, _at(mask), yt, Y.data_ptr(),
-                                          rnorm.data_ptr(), st))
+    index = _place("X mask Y rnorm", X, mask, Y, rnorm)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_normalize_fwd(X, mask, dt, Y, rnorm)
+    if Y is None:
+        Y = torch.empty_like(X, dtype=dt)
+    if rnorm is None:
+        rnorm = torch.empty(lead, dtype=torch.float32, device=X.device)
+    _check("maxsim_normalize_fwd",
+           lib().maxsim_normalize_fwd(xt, X.data_ptr(), T, d, _at(mask), yt, Y.data_ptr(),
+                                      rnorm.data_ptr(), _raw_stream(index)))
     return Y, rnorm
 
 
@@ -741,16 +756,20 @@ def maxsim_normalize_bwd(X: torch.Tensor, rnorm: torch.Tensor, dY: torch.Tensor,
     xt = _row_type("X", X.dtype)
     dt = dX.dtype if dX is not None else X.dtype if out_dtype is None else out_dtype
     gt = _row_type("out_dtype", dt)
-    lead, T, d = _rows("X", X)
+    shape, lead, T, d = _rows("X", X)
     _has("rnorm", rnorm, torch.float32, lead)
-    _has("dY", dY, torch.float32, X.shape)
-    _has("dX", dX, dt, X.shape)
-    with _On(stream, (("X", X), ("rnorm", rnorm), ("dY", dY), ("dX", dX))) as st:
-        if dX is None:
-            dX = torch.empty_like(X, dtype=dt)
-        _check("maxsim_normalize_bwd",
-               lib().maxsim_normalize_bwd(xt, X.data_ptr(), rnorm.data_ptr(), dY.data_ptr(), T, d,
-                                          gt, dX.data_ptr(), st))
+    _has("dY", dY, torch.float32, shape)
+    _has("dX", dX, dt, shape)
+    index = _place("X rnorm dY dX", X, rnorm, dY, dX)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_normalize_bwd(X, rnorm, dY, dt, dX)
+    if dX is None:
+        dX = torch.empty_like(X, dtype=dt)
+    _check("maxsim_normalize_bwd",
+           lib().maxsim_normalize_bwd(xt, X.data_ptr(), rnorm.data_ptr(), dY.data_ptr(), T, d, gt,
+                                      dX.data_ptr(), _raw_stream(index)))
     return dX
 
 
@@ -762,11 +781,15 @@ def _dropout(fn: str, X, p, seed, step, step_dev, Y, stream, names):
     if step_dev is not None and (step_dev.dtype != torch.int64 or step_dev.numel() != 1):
         raise ValueError("step_dev must be one int64")
     _has(names[1], Y, X.dtype, X.shape)
-    with _On(stream, ((names[0], X), ("step_dev", step_dev), (names[1], Y))) as st:
-        if Y is None:
-            Y = torch.empty_like(X)
-        _check(fn, getattr(lib(), fn)(code, X.data_ptr(), X.numel(), float(p), int(seed), int(step),
-                                      _at(step_dev), Y.data_ptr(), st))
+    index = _place(f"{names[0]} step_dev {names[1]}", X, step_dev, Y)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return _dropout(fn, X, p, seed, step, step_dev, Y, None, names)
+    if Y is None:
+        Y = torch.empty_like(X)
+    _check(fn, getattr(lib(), fn)(code, X.data_ptr(), X.numel(), float(p), int(seed), int(step),
+                                  _at(step_dev), Y.data_ptr(), _raw_stream(index)))
     return Y
 
 
