@@ -588,7 +588,7 @@ def _elsewhere(stream, index: int):
 
 # the current stream's handle: building a Stream object takes longer than the
 # call's checks
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _at(t: Optional[torch.Tensor]):

@@ -20,7 +20,8 @@
 // loop on such data reaches 3.4).
 // few_kernel: a few tokens. W is the traffic; every fragment goes straight from
 // memory to registers, waves split k, and LDS joins their sums. One token through
-// 4096 x 4096 weights takes 5.3 us, 2.8 of them the launch.
+// 4096 x 4096 weights takes 5.3 us, 2.8 of them the launch. With join_kernel it
+// also makes embeddings whose channels are spread over workgroups.
 #include <type_traits>
 
 #include "embed_common.hpp"
@@ -190,12 +191,12 @@ struct Rows {
                         const double y = scaled64(sum(tt, b, i), (double)as[tt], w, c);
                         m = __builtin_fmax(m, __builtin_fabs(y));
                         s2 = __builtin_fma(y, y, s2);
-                        if constexpr (kKeep) y64[b * R + i] = y;
+                        if constexpr (kKeep) y64[(tt * NB + b) * R + i] = y;
                     } else {
                         const float y = scaled(sum(tt, b, i), as[tt], w, c);
                         mf = __builtin_fmaxf(mf, __builtin_fabsf(y));
                         s2 = __builtin_fma((double)y, (double)y, s2);
-                        if constexpr (kKeep) y32[b * R + i] = y;
+                        if constexpr (kKeep) y32[(tt * NB + b) * R + i] = y;
                     }
                 });
                 run_ends();
@@ -269,7 +270,7 @@ struct Rows {
                 static_for<0, NB>([&](auto b) {
                     float y[R];
                     static_for<0, R>([&](auto i) {
-                        if constexpr (kKeep) y[i] = y32[b * R + i] * inv * r;
+                        if constexpr (kKeep) y[i] = y32[(tt * NB + b) * R + i] * inv * r;
                         else y[i] = scaled(again(sum(tt, b, i)), as[tt], ws[chan(b) + i], bs[chan(b) + i]) * inv * r;
                     });
                     if (in) store_run<R>(a.Y, a.out, t[tt], chan(b), a.N, y);
@@ -284,7 +285,7 @@ struct Rows {
                     uint32_t q[R];
                     static_for<0, R>([&](auto i) {
                         double y;
-                        if constexpr (kKeep) y = y64[b * R + i];
+                        if constexpr (kKeep) y = y64[(tt * NB + b) * R + i];
                         else y = scaled64(again(sum(tt, b, i)), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
                         q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(y, inv, magic));
                     });
@@ -725,11 +726,17 @@ __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
 // A few tokens
 // ---------------------------------------------------------------------------
 
+// What few_kernel makes of its sums: products, whole normalised rows, or normalised
+// rows whose channels are spread over workgroups (see embed_split).
+enum Few : int { kProduct, kWhole, kStats, kFinish };
+
 // TT tiles of 16 tokens x (NW * NPW) tiles of 16 channels per workgroup; NW
 // waves side by side over the channels, KW waves over k.
-template <int TT, int NPW, int NW, int KW, bool EMBED, bool UNAL>
+template <int TT, int NPW, int NW, int KW, int MODE, bool UNAL>
 __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
 {
+    constexpr bool EMBED = MODE == kWhole, SPLIT = MODE == kStats || MODE == kFinish;
+    static_assert(!SPLIT || (NPW == 1 && NW == 1), "one tile of channels");
     constexpr int BN = NW * NPW * 16;
     __shared__ __align__(16) float ws[BN], bs[BN];
     __shared__ __align__(16) i32x4 sums[KW > 1 ? (KW - 1) * NW * NPW * TT * 64 : 1];
@@ -737,7 +744,7 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int kw = wave / NW, nw = wave % NW;
     const int n0 = EMBED ? 0 : (int)blockIdx.x * BN;
-    const int64_t t0 = EMBED ? (int64_t)blockIdx.x * (TT * 16) : 0;
+    const int64_t t0 = (int64_t)(EMBED ? blockIdx.x : blockIdx.y) * (TT * 16);
     const int row = lane & 15, quarter = lane >> 4;
 
     for (int i = threadIdx.x; i < BN; i += NW * KW * 64) {
@@ -763,7 +770,7 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
         const int64_t t = t0 + j * 16 + row;
         const bool in = t < a.T && kw == 0;
         as[j] = in ? a.a_scale[t] : 0.0f;
-        live[j] = in && (!EMBED || !a.mask || a.mask[t]);
+        live[j] = in && (MODE == kProduct || !a.mask || a.mask[t]);
     }
     i32x4 acc[NPW][TT];
 #pragma unroll
@@ -825,6 +832,51 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
             a, [&](auto j, auto b, auto i) { return acc[b][j][(int)i]; },
             [&](int b) { return (nw * NPW + b) * 16 + quarter * 4; }, ws, bs, t, as, live, slot, kw == 0 ? nw : -1, red,
             TT * 16);
+    } else if constexpr (SPLIT) {
+        if (kw > 0) return;
+        int64_t t[TT];
+        int slot[TT] = {};
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            t[j] = t0 + j * 16 + row;
+            if (!live[j]) as[j] = 0.0f;
+        }
+        auto sum = [&](auto j, auto, auto i) { return acc[0][j][(int)i]; };
+        auto local = [&](int) { return quarter * 4; };
+        const int64_t es = a.out == kI8 ? 1 : a.out == kF32 ? 4 : 2;
+        auto go = [&](auto& rows) {
+            rows.first(sum, local, ws, bs, as, live);
+            if constexpr (MODE == kStats) rows.put(nullptr, 0, slot, 0);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                if (t[j] >= a.T) continue;
+                double* stat = (double*)((char*)a.Y + (t[j] * a.N + n0) * es);
+                if constexpr (MODE == kStats) {
+                    if (quarter == 0) {
+                        stat[0] = rows.top[j];
+                        stat[1] = rows.ss[j];
+                    }
+                } else {
+                    rows.top[j] = stat[0];
+                    rows.ss[j] = stat[1];
+                }
+            }
+            if constexpr (MODE == kFinish) {
+                // the whole wave has its statistics before any lane overwrites them
+                __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+                lds_fence();
+                LinearArgs at = a;  // channels are counted from n0 in ws and bs
+                at.Y = (char*)a.Y + n0 * es;
+                rows.second(at, sum, local, ws, bs, t, as, live, nullptr, 0, slot, n0 == 0 ? 0 : -1);
+            }
+        };
+        if (a.out == kI8) {
+            Rows<true, TT, 1, 4, 16, 1> rows;
+            go(rows);
+        } else {
+            Rows<false, TT, 1, 4, 16, 1> rows;
+            go(rows);
+        }
     } else {
         if (kw > 0) return;
 #pragma unroll
@@ -843,6 +895,29 @@ __global__ __launch_bounds__(NW* KW * 64) void few_kernel(LinearArgs a)
     }
 }
 
+// Joins the statistics that N / 16 workgroups left in each row (lane r those of
+// channels 16 r ..) and leaves the row's in every one of their places. A wave
+// takes a row.
+__global__ __launch_bounds__(256) void join_kernel(LinearArgs a)
+{
+    const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    const int r = threadIdx.x & 63;
+    if (t >= a.T) return;
+    const int64_t es = a.out == kI8 ? 1 : a.out == kF32 ? 4 : 2;
+    double* stat = (double*)((char*)a.Y + (t * a.N + r * 16) * es);
+    const bool has = r * 16 < a.N;
+    double top = has ? stat[0] : 0.0, ss = has ? stat[1] : 0.0;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+        top = __builtin_fmax(top, xor_lane(top, m));
+        ss += xor_lane(ss, m);
+    }
+    if (has) {
+        stat[0] = top;
+        stat[1] = ss;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
@@ -858,12 +933,14 @@ void run_tiles(LinearArgs a, hipStream_t stream)
                        dim3(WT * WN * 64), 0, stream, a);
 }
 
-template <int TT, int NPW, int NW, int KW, bool EMBED>
+template <int TT, int NPW, int NW, int KW, int MODE>
 void run_few(const LinearArgs& a, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(EMBED ? tiles(a.T, TT * 16) : tiles(a.N, NW * NPW * 16))), block(NW * KW * 64);
-    if (a.K % 16 == 0) hipLaunchKernelGGL((few_kernel<TT, NPW, NW, KW, EMBED, false>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((few_kernel<TT, NPW, NW, KW, EMBED, true>), grid, block, 0, stream, a);
+    const unsigned over_t = (unsigned)tiles(a.T, TT * 16);
+    const dim3 grid = MODE == kWhole ? dim3(over_t) : dim3((unsigned)tiles(a.N, NW * NPW * 16), over_t);
+    const dim3 block(NW * KW * 64);
+    if (a.K % 16 == 0) hipLaunchKernelGGL((few_kernel<TT, NPW, NW, KW, MODE, false>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((few_kernel<TT, NPW, NW, KW, MODE, true>), grid, block, 0, stream, a);
 }
 
 // Tiles by how many the launch has (median us of N = K = 4096 bf16 outputs with
@@ -887,8 +964,8 @@ void linear_tiles(const LinearArgs& a, hipStream_t stream)
 
 void linear_once(const LinearArgs& a, hipStream_t stream)
 {
-    if (a.T <= 16) run_few<1, 1, 1, 8, false>(a, stream);
-    else if (a.T <= 32) run_few<2, 1, 1, 8, false>(a, stream);
+    if (a.T <= 16) run_few<1, 1, 1, 8, kProduct>(a, stream);
+    else if (a.T <= 32) run_few<2, 1, 1, 8, kProduct>(a, stream);
     else if (a.K % 16 == 0) linear_tiles<false>(a, stream);
     else linear_tiles<true>(a, stream);
 }
@@ -934,16 +1011,43 @@ void embed_stream(const LinearArgs& a, hipStream_t stream)
     }
 }
 
+// Few tokens, many weights: one CU fills at about 70 B/ns, so one workgroup per
+// block of rows would take W's bytes at that rate. Here every tile of 16 channels
+// has a workgroup: the first launch leaves the tile's statistics of each row in the
+// 16 bytes or more of E that the tile will fill, the second joins a row's, the
+// third forms the sums again (W comes from the caches then) and overwrites its own
+// place. 32 tokens of 1024 to 1024 channels take 10.6 us, 23.7 in tiles of whole
+// rows; of 4096 to 128 17.8 us, 30.9 in the direct form. Three launches cost about
+// 5 us more than one, so it takes over 160,000 weights to pay (1000 to 128 channels
+// 10.6 against 7.2 us, 1536 to 128 11.3 against 13.6), beyond 256 channels, where
+// the other choice is tiles, any number (64 to 512 channels 8.3 against 7.7 us, to
+// 1024 8.5 against 11.0). From 1024 tokens on the tiles are ahead (768 to 768
+// channels 17.7 against 23.2 us; 512 tokens 17.4 against 15.3).
+constexpr int64_t kSplitTokens = 512, kSplitWeights = 160000;
+bool split_ok(const LinearArgs& a)
+{
+    return a.T <= kSplitTokens && a.N % 16 == 0 && (a.N > 256 || (int64_t)a.N * a.K > kSplitWeights);
+}
+void embed_split(const LinearArgs& a, hipStream_t stream)
+{
+    if (a.T <= 16) run_few<1, 1, 1, 8, kStats>(a, stream);
+    else run_few<2, 1, 1, 8, kStats>(a, stream);
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)tiles(a.T, 4)), dim3(256), 0, stream, a);
+    if (a.T <= 16) run_few<1, 1, 1, 8, kFinish>(a, stream);
+    else run_few<2, 1, 1, 8, kFinish>(a, stream);
+}
+
 // The streamed form where it fits, at any number of tokens (1 to 4096 tokens of
-// 768 to 128 channels 6.7 to 7.1 us; direct form 8.7 to 9.2, tiles 12.7 to 14.1).
-// Elsewhere few tokens take the direct form up to 256 channels (4096 tokens of
-// 2048 to 128 channels 18.3 us, tiles 27.8) and tiles beyond, where one workgroup
-// reads too many weights (32 tokens of 1024 to 1024 channels 25.7 us, direct 40.4).
+// 768 to 128 channels 6.0 to 7.1 us; direct form 8.7 to 9.2, tiles 12.7 to 14.1).
+// Elsewhere few tokens spread their channels over workgroups if the weights are
+// many, or take the direct form up to 256 channels (4096 tokens of 2048 to 128
+// channels 18.3 us, tiles 27.8), and tiles beyond.
 void embed_once(const LinearArgs& a, hipStream_t stream)
 {
     if (stream_ok(a)) return embed_stream(a, stream);
-    if (a.T <= 4096 && a.N <= 128) return run_few<1, 1, 8, 2, true>(a, stream);
-    if (a.T <= 4096 && a.N <= 256) return run_few<1, 1, 16, 1, true>(a, stream);
+    if (split_ok(a)) return embed_split(a, stream);
+    if (a.T <= 4096 && a.N <= 128) return run_few<1, 1, 8, 2, kWhole>(a, stream);
+    if (a.T <= 4096 && a.N <= 256) return run_few<1, 1, 16, 1, kWhole>(a, stream);
     if (a.K % 16 == 0) embed_tiles<false>(a, stream);
     else embed_tiles<true>(a, stream);
 }

@@ -339,6 +339,9 @@ EMBED = [
     (4500, 48, 300), (5000, 96, 77), (4200, 200, 256), (6000, 256, 400), (4300, 300, 96),
     (4100, 512, 1040), (4099, 513, 64), (5001, 1024, 320), (4098, 770, 130), (4200, 5, 33),
     (4120, 384, 72), (70, 600, 1000), (33, 768, 4096), (300, 128, 4096), (4200, 128, 8192), (4300, 250, 2049),
+    # few tokens, wide rows: their channels spread over workgroups
+    (32, 512, 1024), (100, 768, 300), (256, 1024, 77), (17, 272, 4096), (200, 1008, 33), (1, 1024, 64), (257, 784, 48),
+    (32, 128, 2048), (512, 64, 4096), (513, 272, 600), (33, 256, 1001), (5, 16, 12000), (512, 1024, 200),
     # many tokens, a projection that stays in registers: every depth and width class
     (5000, 96, 128), (4999, 128, 384), (9000, 40, 640), (4111, 128, 1024), (40000, 128, 768),
     (4500, 130, 256), (4100, 256, 512), (9001, 250, 896), (5003, 200, 768), (20000, 256, 1024),
@@ -635,7 +638,9 @@ def test_training_run_gradient(ms):
 def test_bitwise_repeatable(ms):
     x = _rows(5000, 768, torch.bfloat16, 61)
     a, s, w, ws, b = _operands(5000, 384, 768, 62)
+    few = _operands(40, 1024, 512, 63)
     for call in (lambda: ms.maxsim_quantize_tok(x, normalize=True), lambda: ms.maxsim_normalize_fwd(x),
+                 lambda: ms.maxsim_embed_i8(*few),
                  lambda: ms.maxsim_embed_i8(a, s, w, ws, b), lambda: (ms.maxsim_linear_i8(a, s, w, ws, b),) * 2):
         first, again = call(), call()
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
