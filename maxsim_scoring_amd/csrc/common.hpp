@@ -184,11 +184,15 @@ __device__ __forceinline__ void block_barrier()
 // treating the load as an LDS write it must wait for before every later LDS
 // access; callers synchronise explicitly with wait_vmcnt. M0 is set here; no
 // compiler-generated code in these kernels keeps a value in M0.
+// The compiler does not look into assembly for hazards, so the block holds the
+// wait states itself: the load needs one behind the scalar write of M0, and five
+// behind a vector instruction that wrote a register of its base (readfirstlane, a
+// spill's readlane); the write of M0 and the s_nop 3 make five.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma_lds16(const void* base, uint32_t voff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(voff), "s"(base)
                  : "memory", "m0");
@@ -196,7 +200,7 @@ __device__ __forceinline__ void dma_lds16(const void* base, uint32_t voff, uint3
 // the same with the non-temporal hint, for data that is streamed once
 __device__ __forceinline__ void dma_lds16_nt(const void* base, uint32_t voff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 nt"
                  :
                  : "s"(lds), "v"(voff), "s"(base)
                  : "memory", "m0");
@@ -205,7 +209,7 @@ __device__ __forceinline__ void dma_lds16_nt(const void* base, uint32_t voff, ui
 // (active lanes only).
 __device__ __forceinline__ void dma_lds4(const void* base, uint32_t voff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2"
                  :
                  : "s"(lds), "v"(voff), "s"(base)
                  : "memory", "m0");
