@@ -165,9 +165,10 @@ maxsim_status_t maxsim_fwd_pairs(maxsim_dtype_t dtype, const void* Q, const void
 
 /*
  * Top-k after scoring (TileMaxSim paper, Sec. 6.8 "End-to-End Retrieval
- * Latency"): for each row i of scores [Nq, Nd] float32 (no NaN), the K
- * largest values in decreasing order; equal values are taken in increasing
- * column order (-0 and +0 are equal).
+ * Latency"): for each row i of scores [Nq, Nd] float32, the K largest values
+ * in decreasing order; equal values are taken in increasing column order (-0
+ * and +0 are equal). A NaN counts as larger than +Inf, or as smaller than -Inf
+ * if its sign bit is set.
  *   ids  [Nq, Nd] int32 or NULL: idx reports ids[i, column] instead of the
  *        column (e.g. the doc ids of a candidate list)
  *   idx  [Nq, K] int32, val [Nq, K] float32 (the input values, bit for bit)

@@ -37,10 +37,11 @@ FLAGS = [
 # accumulation registers (no copy back per MFMA); the other kernels keep the
 # compiler's default register form. The embedding head carries activations and
 # gradients, where an overflow upstream must stay visible: NaNs are honoured
-# there (later flags win).
+# there (later flags win). They are in the top-k too, which keeps k candidates
+# whatever the scores hold.
 _NANS = ["-Xarch_device", "-fhonor-nans", "-Xarch_device", "-mamdgpu-ieee"]
 EXTRA = {"chamfer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "embed_rows.hip": _NANS, "embed_linear.hip": _NANS}
+         "topk.hip": _NANS, "embed_rows.hip": _NANS, "embed_linear.hip": _NANS}
 
 
 def _run(cmd, verbose):

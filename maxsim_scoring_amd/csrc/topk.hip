@@ -16,6 +16,10 @@
 // first ones equal to T in doc order are sorted. If the candidates do not fit
 // in LDS, the same select-and-gather runs over the whole row. Output values
 // are re-read from the scores, so they are the input bits exactly.
+//
+// A NaN is a candidate like any other (the test is "not below the threshold", in
+// a file compiled with NaNs honoured), so there are never fewer than k of them.
+// Its key puts it above +Inf, or below -Inf if its sign bit is set.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -243,7 +247,7 @@ __global__ __launch_bounds__(kTkThreads) void topk_kernel(TopkArgs a)
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int64_t j = c0 + 64 * u + lane;
-            const bool take = j < c_hi && v[u] >= theta;
+            const bool take = j < c_hi && !(v[u] < theta);
             const uint64_t bal = __ballot(take);
             if (bal == 0) continue;  // uniform: the common case
             if (take) {

@@ -1,0 +1,52 @@
+"""Values at the ends of the float types on the GPU: NaN, infinities, the largest
+and smallest magnitudes, exact ties."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def ms():
+    import maxsim_scoring_amd as m
+    m.binding.lib()
+    assert torch.cuda.is_available()
+    return m
+
+
+# --------------------------------------------------------------------- top-k
+
+def _ranked(v):
+    """Columns in decreasing order of the values: positive NaN, +Inf ... -Inf,
+    negative NaN (each by its bits), equal values by column."""
+    b = v.view(np.uint32).astype(np.int64)
+    b = np.where((b & 0x7FFFFFFF) == 0, 0, b)
+    key = np.where(b & 0x80000000, 0xFFFFFFFF - b, b | 0x80000000)
+    return np.lexsort((np.arange(len(v)), -key))
+
+
+@pytest.mark.parametrize("Nd,k", [(5, 5), (64, 20), (8192, 100), (8193, 100), (30000, 1000), (100000, 100)])
+def test_topk_with_nans(ms, Nd, k):
+    """Rows with some NaN, with fewer than k other values, and with nothing else:
+    every index is a column of the row, once, and in order."""
+    rng = np.random.default_rng(Nd)
+    v = rng.standard_normal((6, Nd)).astype(np.float32)
+    v[0, ::3] = np.nan
+    v[1, k - 1:] = np.nan                       # one value fewer than k
+    v[2] = np.nan
+    v[3] = np.array(0xFFC00000, np.uint32).view(np.float32)  # the sign bit set: below -Inf
+    v[4, 1:] = np.array(0xFFFFFFFF, np.uint32).view(np.float32)
+    v[4, -1] = -np.inf
+    v[5, 1::2] = np.nan
+    v[5, 3::4] = -np.inf
+    s = torch.from_numpy(v).to(DEV)
+    idx, val, rows = ms.maxsim_topk(s, k, want_rows=True)
+    want = np.stack([_ranked(r)[:k] for r in v])
+    assert np.array_equal(idx.cpu().numpy(), want)
+    got = val.cpu().numpy().view(np.uint32)
+    assert np.array_equal(got, np.take_along_axis(v, want, 1).view(np.uint32))
+    assert np.array_equal(rows.cpu().numpy(), np.repeat(np.arange(6), k).reshape(6, k))
