@@ -110,8 +110,8 @@ struct Max { __device__ __forceinline__ float operator()(float a, float b) const
 // What the codes of a row need beside its values.
 struct Quant {
     float top;   // largest magnitude
-    float inv;   // about 127 / top
-    float near;  // how far from an integer a code is decided in float64
+    float inv;   // about 127 / top; 0 where every code is decided in float64
+    float near;  // how far from an integer a code is decided in float64, -1: always
     bool zero;
 };
 __device__ __forceinline__ Quant quant_of(float top)
@@ -119,8 +119,9 @@ __device__ __forceinline__ Quant quant_of(float top)
     Quant s;
     s.top = top;
     s.zero = !(top >= kTiny);
-    s.inv = s.zero ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(top);
-    s.near = top < 0x1p120f ? 0.5f - 0x1p-14f : -1.0f;  // the reciprocal of larger ones vanishes
+    const bool large = top >= 0x1p120f;  // the reciprocal vanishes from 2^126 on
+    s.inv = s.zero || large ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(top);
+    s.near = large ? -1.0f : 0.5f - 0x1p-14f;
     return s;
 }
 
@@ -151,7 +152,7 @@ __device__ __forceinline__ void make_codes(const float (&x)[C], const Quant& s, 
 #pragma unroll
         for (int i = 0; i < C; ++i)
             b[i] = (uint32_t)(int)__builtin_rint((double)x[i] * 127.0 / (double)s.top);
-        if (SQUARES && s.near < 0.0f) {
+        if (SQUARES && s.near < 0.0f) {  // the values above were x * 0
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const float v = (float)((double)x[i] * 127.0 / (double)s.top);

@@ -5,6 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+import embed_reference as ref
+from embed_reference import f64
+
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
@@ -50,3 +53,26 @@ def test_topk_with_nans(ms, Nd, k):
     got = val.cpu().numpy().view(np.uint32)
     assert np.array_equal(got, np.take_along_axis(v, want, 1).view(np.uint32))
     assert np.array_equal(rows.cpu().numpy(), np.repeat(np.arange(6), k).reshape(6, k))
+
+
+# -------------------------------------------------------------- quantisation
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d", [96, 100, 768, 1030, 9001, 16640])
+def test_quantize_rows_of_large_magnitude(ms, d, dtype):
+    """Largest magnitudes on both sides of 2^120, from which on codes are always
+    decided in float64, and of 2^126, from which on the reciprocal is subnormal.
+    The scale's bound is that of ordinary rows: every value is rounded once more
+    or once less before it is squared, well within the 3 of test_quantize."""
+    g = torch.Generator(device=DEV).manual_seed(d)
+    tops = [2.0 ** e for e in (100, 119, 119.99, 120, 120.5, 123, 125.9, 125.999, 126, 126.1, 127.9)]
+    x = torch.rand(len(tops), d, generator=g, device=DEV, dtype=torch.float64) * 2 - 1
+    x /= x.abs().amax(1, keepdim=True)
+    x = (x * torch.tensor(tops, device=DEV, dtype=torch.float64)[:, None]).to(dtype)
+    for normalize in (False, True):
+        codes, scale = ms.maxsim_quantize_tok(x, normalize=normalize)
+        want, ws, _ = ref.quantize(f64(x), None, normalize)
+        assert np.array_equal(codes.cpu().numpy(), want)
+        bound = np.abs(ws) * (((ref.depth(d) + 3) / 2 + 3 if normalize else 1) * 1.01 * ref.U)
+        off = np.abs(f64(scale) - ws)
+        assert (off <= bound).all(), (normalize, (f64(scale) / ws).tolist())
