@@ -53,7 +53,8 @@ extern "C" {
  * positive).
  *   X [T, d] of `dtype` (F16, BF16, F32); mask [T] or NULL
  *   codes int8 [T, d] in [-127, 127], scale float32 [T]: fully overwritten
- * Values of X are finite (others give unspecified codes in their own row).
+ * A row that holds a NaN or an infinity (and is not masked) gets scale NaN and
+ * unspecified codes, so that whatever is computed from it is NaN.
  * Errors: SHAPE (negative sizes), UNSUPPORTED (d outside 1..131071, dtype,
  * alignment), NULL, OVERFLOW (T >= 2^31).
  */

@@ -102,6 +102,8 @@ __device__ __forceinline__ float group_reduce(float v, OP op)
 }
 struct Add { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
 struct Max { __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_fmaxf(a, b); } };
+// The maximum that is NaN where either operand is (v_maximum3_f32).
+struct MaxNan { __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); } };
 
 // ---------------------------------------------------------------------------
 // Quantisation
@@ -111,17 +113,18 @@ struct Max { __device__ __forceinline__ float operator()(float a, float b) const
 struct Quant {
     float top;   // largest magnitude
     float inv;   // about 127 / top; 0 where every code is decided in float64
-    float near;  // how far from an integer a code is decided in float64, -1: always
+    float near;  // how far from an integer a code is decided in float64, -1: always, 1: never
     bool zero;
 };
 __device__ __forceinline__ Quant quant_of(float top)
 {
     Quant s;
     s.top = top;
-    s.zero = !(top >= kTiny);
-    const bool large = top >= 0x1p120f;  // the reciprocal vanishes from 2^126 on
+    s.zero = top < kTiny;
+    const bool large = !(top < 0x1p120f);  // the reciprocal vanishes from 2^126 on
     s.inv = s.zero || large ? 0.0f : 127.0f * __builtin_amdgcn_rcpf(top);
-    s.near = large ? -1.0f : 0.5f - 0x1p-14f;
+    // a NaN or an infinity leaves the codes open; the scale comes out as NaN
+    s.near = !large ? 0.5f - 0x1p-14f : top <= 0x1.fffffep127f ? -1.0f : 1.0f;
     return s;
 }
 
@@ -148,7 +151,7 @@ __device__ __forceinline__ void make_codes(const float (&x)[C], const Quant& s, 
         off = __builtin_fmaxf(off, __builtin_fabsf(v - (m - kMagic)));
         if (SQUARES) ss = __builtin_fmaf(v, v, ss);
     }
-    if (off >= s.near && !s.zero) {
+    if (off >= s.near) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
             b[i] = (uint32_t)(int)__builtin_rint((double)x[i] * 127.0 / (double)s.top);
@@ -182,6 +185,8 @@ __device__ __forceinline__ void store_codes(void* Y, int64_t at, const uint32_t 
 }
 
 // top / 127: the product with 1/127 and one correction step; or 1 / sqrt(ss).
+// Both are NaN where the row holds a NaN (top and ss are) or an infinity (top is
+// one, and x * inv is Inf * 0).
 __device__ __forceinline__ float quant_scale(const Quant& s, bool normalize, float ss)
 {
     if (s.zero) return 1.0f;
@@ -210,9 +215,9 @@ __device__ __forceinline__ void quantize_rows(const RowArgs& a)
             float x[C];
             unpack<E, VB>(raw[j], x);
 #pragma unroll
-            for (int i = 0; i < C; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(x[i]));
+            for (int i = 0; i < C; ++i) top = MaxNan{}(top, __builtin_fabsf(x[i]));
         }
-        const Quant s = quant_of(group_reduce<G>(top, Max{}));
+        const Quant s = quant_of(group_reduce<G>(top, MaxNan{}));
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
@@ -252,10 +257,10 @@ __global__ __launch_bounds__(kThreads) void quantize_long_kernel(RowArgs a)
                 float x[C];
                 unpack<E, VB>(src[c], x);
 #pragma unroll
-                for (int i = 0; i < C; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(x[i]));
+                for (int i = 0; i < C; ++i) top = MaxNan{}(top, __builtin_fabsf(x[i]));
             }
         }
-        const Quant s = quant_of(group_reduce<64>(top, Max{}));
+        const Quant s = quant_of(group_reduce<64>(top, MaxNan{}));
         float ss = 0.0f;
 #pragma unroll 4
         for (int c = lane; c < nv; c += 64) {

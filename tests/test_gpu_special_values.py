@@ -76,3 +76,39 @@ def test_quantize_rows_of_large_magnitude(ms, d, dtype):
         bound = np.abs(ws) * (((ref.depth(d) + 3) / 2 + 3 if normalize else 1) * 1.01 * ref.U)
         off = np.abs(f64(scale) - ws)
         assert (off <= bound).all(), (normalize, (f64(scale) / ws).tolist())
+
+
+WRONG = [float("nan"), float("inf"), -float("inf")]
+
+
+def _spoiled(T, d, dtype, seed):
+    """Ordinary rows and the same rows with a NaN or an infinity in some of them
+    (row 1 NaN throughout, row 4 masked): (clean, spoiled, mask, spoiled rows)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(T, d, generator=g, device=DEV).to(dtype)
+    y = x.clone()
+    y[1] = float("nan")
+    for i, w in enumerate(WRONG):
+        y[6 + i, (7 * i) % d] = w
+    y[9, d - 1] = float("nan")
+    y[9, 0] = float("inf")
+    y[4] = float("nan")
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+    mask[4] = 0
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    bad[[1, 6, 7, 8, 9]] = True
+    return x, y, mask, bad
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [1, 7, 8, 100, 128, 768, 1030, 9001, 16640])
+def test_quantize_shows_nan_and_inf(ms, d, dtype):
+    """What a row with a NaN or an infinity stands for is NaN; masked rows and all
+    others are as without them."""
+    x, y, mask, bad = _spoiled(70, d, dtype, d)
+    for normalize in (False, True):
+        codes, scale = ms.maxsim_quantize_tok(y, mask, normalize=normalize)
+        want, ws = ms.maxsim_quantize_tok(x, mask, normalize=normalize)
+        assert torch.isnan(codes * scale[:, None])[bad].all(), normalize
+        assert torch.equal(codes[~bad], want[~bad]) and torch.equal(scale[~bad], ws[~bad])
+        assert scale[4] == 1 and not codes[4].any()
