@@ -89,6 +89,8 @@ maxsim_status_t maxsim_linear_i8(maxsim_dtype_t dtype, const int8_t* A, const fl
  * dtype I8: E int8 [T, d] codes of y[t] and e_scale float32 [T], as
  *   maxsim_quantize_tok with normalize makes them of y (y and the codes are
  *   computed in float64). Rows of zeros and masked rows give codes 0, scale 1.
+ * A row whose y holds a NaN or an infinity gives NaN: as floats in every
+ * channel, as codes (unspecified) through scale NaN.
  * E holds scratch until it is written.
  *   mask [T] uint8 or NULL; a mask needs no care for what A and a_scale hold
  *   in the rows it drops.

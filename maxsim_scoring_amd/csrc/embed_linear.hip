@@ -259,11 +259,12 @@ struct Rows {
                 }
             }
         }
-        // zero rows are multiplied by 0: their values are finite
+        // zero rows are multiplied by 0: their values are finite. top leaves NaNs out,
+        // ss does not: a row with one is no zero row, and its scale is NaN.
         static_for<0, TT>([&](auto tt) {
             const bool in = t[tt] < a.T;
+            const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
             if constexpr (!CODES) {
-                const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
                 const float inv = zero ? 0.0f : 1.0f / (float)top[tt];
                 // the rest of the norm is between 1 and the square root of N
                 const float r = zero ? 0.0f : rsqrt_f((float)(ss[tt] * (double)inv * (double)inv));
@@ -277,7 +278,6 @@ struct Rows {
                     run_ends();
                 });
             } else {
-                const bool zero = !(top[tt] >= (double)kTiny);
                 const double inv = zero ? 0.0 : 127.0 / top[tt];
                 double magic = 0x1.8p52;
                 asm("" : "+v"(magic));  // a register: as a constant it is copied for every fma

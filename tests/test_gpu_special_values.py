@@ -112,3 +112,57 @@ def test_quantize_shows_nan_and_inf(ms, d, dtype):
         assert torch.isnan(codes * scale[:, None])[bad].all(), normalize
         assert torch.equal(codes[~bad], want[~bad]) and torch.equal(scale[~bad], ws[~bad])
         assert scale[4] == 1 and not codes[4].any()
+
+
+# ------------------------------------------------------------------ products
+
+# T, d, K of every form of maxsim_embed_i8: streamed (4 and 8 waves), direct (8 and
+# 16 waves), channels spread over workgroups, tiles of every width class, rows at
+# any address
+FORMS = [(40, 128, 768), (70, 100, 256), (40, 250, 384), (33, 100, 130), (40, 200, 96), (40, 512, 1024),
+         (12, 272, 4096), (4120, 40, 48), (4120, 200, 272), (520, 300, 96), (600, 700, 64), (513, 1000, 77)]
+forms = pytest.mark.parametrize("T,d,K", FORMS)
+
+
+def _operands(T, d, K, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    a = torch.randint(-128, 128, (T, K), generator=g, device=DEV, dtype=torch.int8)
+    w = torch.randint(-128, 128, (d, K), generator=g, device=DEV, dtype=torch.int8)
+    s = torch.exp(torch.randn(T, generator=g, device=DEV)) / 127
+    ws = torch.exp(torch.randn(d, generator=g, device=DEV)) / (127 * K ** 0.5)
+    return a, s, w, ws, torch.randn(d, generator=g, device=DEV)
+
+
+@forms
+def test_embed_shows_nan_and_inf(ms, T, d, K):
+    """A row whose scale is NaN or infinite stands for NaN, in floats and in codes;
+    all other rows are as without it."""
+    a, s, w, ws, b = _operands(T, d, K, T + d + K)
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    bad[torch.tensor([1, 5, T - 1], device=DEV)] = True
+    spoiled = s.clone()
+    spoiled[bad] = torch.tensor(WRONG, device=DEV)
+    for bias in (None, b):
+        codes, scale = ms.maxsim_embed_i8(a, spoiled, w, ws, bias)
+        want, wscale = ms.maxsim_embed_i8(a, s, w, ws, bias)
+        assert torch.isnan(codes * scale[:, None])[bad].all()
+        assert torch.equal(codes[~bad], want[~bad]) and torch.equal(scale[~bad], wscale[~bad])
+        for out in (torch.float16, torch.bfloat16, torch.float32):
+            e, _ = ms.maxsim_embed_i8(a, spoiled, w, ws, bias, out_dtype=out)
+            want, _ = ms.maxsim_embed_i8(a, s, w, ws, bias, out_dtype=out)
+            assert torch.isnan(e[bad]).all() and torch.equal(e[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("K", [768, 100, 4096])
+def test_hidden_states_with_nan_and_inf(ms, K, dtype):
+    """From hidden states to embeddings: broken states give NaN, masked ones zeros."""
+    x, y, mask, bad = _spoiled(70, K, dtype, K)
+    _, _, w, ws, b = _operands(1, 128, K, K)
+    codes, scale = ms.embed_tokens_i8(y, w, ws, b, mask)
+    want, wscale = ms.embed_tokens_i8(x, w, ws, b, mask)
+    assert torch.isnan(codes * scale[:, None])[bad].all()
+    assert torch.equal(codes[~bad], want[~bad]) and torch.equal(scale[~bad], wscale[~bad])
+    assert scale[4] == 1 and not codes[4].any()
+    e, _ = ms.embed_tokens_i8(y, w, ws, b, mask, out_dtype=torch.bfloat16)
+    assert torch.isnan(e[bad]).all() and torch.isfinite(e[~bad]).all() and not e[4].any()
