@@ -77,21 +77,26 @@ __device__ __forceinline__ double scaled64(int acc, double as, float ws, float b
 }
 
 // R (4 or 16) consecutive outputs n .. n + R - 1 of row t, those below N, in
-// pieces of up to 16 bytes where N keeps every row aligned for them.
+// pieces of up to 16 bytes where N keeps every row aligned for them. zero:
+// zeros in place of y, whatever it holds.
 template <int R>
-__device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, int N, const float (&y)[R])
+__device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, int N, const float (&y)[R],
+                                          bool zero = false)
 {
     const int64_t at = t * N + n;
     if (out == kF32) {
         float* p = (float*)Y + at;
+        float v[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) v[i] = zero ? 0.0f : y[i];
         if ((N & 3) == 0) {
 #pragma unroll
             for (int i = 0; i < R / 4; ++i)
-                if (n + 4 * i < N) ((f32x4*)p)[i] = f32x4{y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
+                if (n + 4 * i < N) ((f32x4*)p)[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i)
-                if (n + i < N) p[i] = y[i];
+                if (n + i < N) p[i] = v[i];
         }
         return;
     }
@@ -104,6 +109,8 @@ __device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, in
 #pragma unroll
         for (int i = 0; i < R / 2; ++i) w[i] = half_pair<kF16>(y[2 * i], y[2 * i + 1]);
     }
+#pragma unroll
+    for (int i = 0; i < R / 2; ++i) w[i] = zero ? 0 : w[i];
     if (R == 16 && (N & 7) == 0) {
 #pragma unroll
         for (int i = 0; i < R / 8; ++i)
@@ -120,15 +127,17 @@ __device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, in
 }
 // The same for codes, each in the low byte of a word.
 template <int R>
-__device__ __forceinline__ void store_codes(void* Y, int64_t t, int n, int N, const uint32_t (&q)[R])
+__device__ __forceinline__ void store_codes(void* Y, int64_t t, int n, int N, const uint32_t (&q)[R], bool zero)
 {
     int8_t* p = (int8_t*)Y + t * N + n;
-    if ((N & 3) == 0) {
-        uint32_t w[R / 4];
+    uint32_t w[R / 4];
 #pragma unroll
-        for (int i = 0; i < R / 4; ++i)
-            w[i] = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0c0c0400u) |
-                   __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x0c0c0400u) << 16;
+    for (int i = 0; i < R / 4; ++i) {
+        w[i] = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0c0c0400u) |
+               __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x0c0c0400u) << 16;
+        w[i] = zero ? 0 : w[i];
+    }
+    if ((N & 3) == 0) {
         if (R == 16 && (N & 15) == 0) {
             if (n < N) *(u32x4*)p = u32x4{w[0], w[R / 4 > 1 ? 1 : 0], w[R / 4 > 2 ? 2 : 0], w[R / 4 > 3 ? 3 : 0]};
         } else {
@@ -140,7 +149,7 @@ __device__ __forceinline__ void store_codes(void* Y, int64_t t, int n, int N, co
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        if (n + i < N) p[i] = (int8_t)q[i];
+        if (n + i < N) p[i] = (int8_t)(w[i / 4] >> 8 * (i % 4));
 }
 
 // f(integral_constant<int, I>) for I = B .. E-1, unrolled at compile time
@@ -259,8 +268,9 @@ struct Rows {
                 }
             }
         }
-        // zero rows are multiplied by 0: their values are finite. top leaves NaNs out,
-        // ss does not: a row with one is no zero row, and its scale is NaN.
+        // top leaves NaNs out, ss does not: a row with one is no zero row, and its
+        // scale is NaN. Masked rows are zeros whatever the weights' scales and the
+        // biases make of them.
         static_for<0, TT>([&](auto tt) {
             const bool in = t[tt] < a.T;
             const bool zero = !live[tt] || (top[tt] < (double)kTiny && !(ss[tt] != ss[tt]));
@@ -274,7 +284,7 @@ struct Rows {
                         if constexpr (kKeep) y[i] = y32[(tt * NB + b) * R + i] * inv * r;
                         else y[i] = scaled(again(sum(tt, b, i)), as[tt], ws[chan(b) + i], bs[chan(b) + i]) * inv * r;
                     });
-                    if (in) store_run<R>(a.Y, a.out, t[tt], chan(b), a.N, y);
+                    if (in) store_run<R>(a.Y, a.out, t[tt], chan(b), a.N, y, zero);
                     run_ends();
                 });
             } else {
@@ -289,7 +299,7 @@ struct Rows {
                         else y = scaled64(again(sum(tt, b, i)), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
                         q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(y, inv, magic));
                     });
-                    if (in) store_codes<R>(a.Y, t[tt], chan(b), a.N, q);
+                    if (in) store_codes<R>(a.Y, t[tt], chan(b), a.N, q, zero);
                     run_ends();
                 });
                 // codes * scale is y / ||y||, so scale = 1 / ||127 y / s||

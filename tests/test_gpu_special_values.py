@@ -166,3 +166,23 @@ def test_hidden_states_with_nan_and_inf(ms, K, dtype):
     assert scale[4] == 1 and not codes[4].any()
     e, _ = ms.embed_tokens_i8(y, w, ws, b, mask, out_dtype=torch.bfloat16)
     assert torch.isnan(e[bad]).all() and torch.isfinite(e[~bad]).all() and not e[4].any()
+
+
+@forms
+def test_masked_rows_are_zeros_whatever_the_weights_hold(ms, T, d, K):
+    """A scale or bias of one channel that is NaN or infinite spoils every row but
+    the masked ones, which are written as zeros."""
+    a, s, w, ws, b = _operands(T, d, K, 3 * T + d + K)
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+    mask[torch.tensor([0, 3, T - 2], device=DEV)] = 0
+    out_of = mask == 0
+    for i, wrong in enumerate(WRONG):
+        for spoil_bias in (False, True):
+            ws2, b2 = ws.clone(), b.clone()
+            (b2 if spoil_bias else ws2)[(5 * i) % d] = wrong
+            for out in (torch.float16, torch.bfloat16, torch.float32):
+                e, _ = ms.maxsim_embed_i8(a, s, w, ws2, b2, mask, out_dtype=out)
+                assert (e[out_of] == 0).all() and torch.isnan(e[~out_of]).any(1).all()
+            codes, scale = ms.maxsim_embed_i8(a, s, w, ws2, b2, mask)
+            assert not codes[out_of].any() and (scale[out_of] == 1).all()
+            assert torch.isnan(scale[~out_of]).all()
