@@ -87,8 +87,10 @@ maxsim_status_t maxsim_linear_i8(maxsim_dtype_t dtype, const int8_t* A, const fl
  * dtype F16, BF16 or F32: E [T, d] of that type, e_scale unused (NULL).
  *   Rows of zeros and masked rows give zeros.
  * dtype I8: E int8 [T, d] codes of y[t] and e_scale float32 [T], as
- *   maxsim_quantize_tok with normalize makes them of y (y and the codes are
- *   computed in float64). Rows of zeros and masked rows give codes 0, scale 1.
+ *   maxsim_quantize_tok with normalize makes them of y: y is the exact sum
+ *   times the exact product of the scales plus the bias, rounded once to
+ *   float64, and its codes are decided exactly, ties to even. Rows of zeros
+ *   and masked rows give codes 0, scale 1.
  * A row whose y holds a NaN or an infinity gives NaN: as floats in every
  * channel, as codes (unspecified) through scale NaN.
  * E holds scratch until it is written.

@@ -31,6 +31,7 @@ namespace maxsim {
 
 namespace {
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
 
 // 16 bytes of a row of K bytes from byte k on (k a multiple of 16); bytes past
@@ -73,7 +74,7 @@ __device__ __forceinline__ float scaled(int acc, float as, float ws, float b)
 }
 __device__ __forceinline__ double scaled64(int acc, double as, float ws, float b)
 {
-    return (double)acc * (as * (double)ws) + (double)b;
+    return __builtin_fma((double)acc, as * (double)ws, (double)b);  // the scales' product is exact
 }
 
 // R (4 or 16) consecutive outputs n .. n + R - 1 of row t, those below N, in
@@ -125,18 +126,11 @@ __device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, in
             if (n + i < N) p[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
     }
 }
-// The same for codes, each in the low byte of a word.
+// The same for codes, four in a word.
 template <int R>
-__device__ __forceinline__ void store_codes(void* Y, int64_t t, int n, int N, const uint32_t (&q)[R], bool zero)
+__device__ __forceinline__ void store_codes(void* Y, int64_t t, int n, int N, const uint32_t (&w)[R / 4])
 {
     int8_t* p = (int8_t*)Y + t * N + n;
-    uint32_t w[R / 4];
-#pragma unroll
-    for (int i = 0; i < R / 4; ++i) {
-        w[i] = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0c0c0400u) |
-               __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x0c0c0400u) << 16;
-        w[i] = zero ? 0 : w[i];
-    }
     if ((N & 3) == 0) {
         if (R == 16 && (N & 15) == 0) {
             if (n < N) *(u32x4*)p = u32x4{w[0], w[R / 4 > 1 ? 1 : 0], w[R / 4 > 2 ? 2 : 0], w[R / 4 > 3 ? 3 : 0]};
@@ -164,6 +158,37 @@ __device__ __forceinline__ void static_for(F&& f)
 
 __device__ __forceinline__ double xor_lane(double v, int m) { return __shfl_xor(v, m, 64); }
 
+// The code of y in byte 2 of a word, inv about 127 / s: the fma adds 1/2 to
+// 127 y / s, and 1.5 * 2^36, which leaves 16 bits of fraction in the low half.
+// inv's rounding moves the sum by 2^-46 and the fma's by 2^-17, so the byte is the
+// integer below the true sum unless those 16 bits are 0. Then (one value in 2^16,
+// and every tie) tie_word decides.
+__device__ __forceinline__ uint32_t code_word(double y, double inv, double magic)
+{
+    return (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(y, inv, magic));
+}
+constexpr double kCodeMagic = 0x1.8p36 + 0.5;
+
+// Byte 2 of `word`, m, or m - 1: which of them is nearest to 127 y / s, the even
+// one on a tie. 254 y and (2 m - 1) s differ by less than 2^-15 of either, so their
+// difference is exact in two parts: that of the rounded products, and that of
+// what rounding took from them (both products have 61 bits).
+__device__ __forceinline__ uint32_t tie_word(uint32_t word, double y, double s)
+{
+#pragma clang fp contract(off)
+    const int m = (int)(word << 8) >> 24;
+    const double c = (double)(2 * m - 1), p = 254.0 * y, q = c * s;
+    const double over = (p - q) + (__builtin_fma(254.0, y, -p) - __builtin_fma(c, s, -q));
+    const bool up = over > 0.0 || (over == 0.0 && (m & 1) == 0);
+    return (uint32_t)(up ? m : m - 1) << 16;
+}
+
+// Four codes in a word.
+__device__ __forceinline__ uint32_t pack_codes(const uint32_t (&q)[4])
+{
+    return __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0602u) | __builtin_amdgcn_perm(q[3], q[2], 0x0c0c0602u) << 16;
+}
+
 // The sums of one call, normalised and written in two halves with a barrier
 // between them. For each of TT tokens a lane holds NB runs of R consecutive
 // channels: sum(tt, b, i) is the int32 sum of channel chan(b) + i.
@@ -173,9 +198,7 @@ __device__ __forceinline__ double xor_lane(double v, int m) { return __shfl_xor(
 // With s the largest magnitude of the row, its values over the norm are
 // (y / s) / ||y / s||, whose factors neither overflow nor vanish; the sum of
 // squares is a float64, which holds the square of every float32 y. Codes are
-// the nearest integers to 127 y / s: y and s are float64 there, so that a value
-// next to the middle between two codes is not moved across it, and adding
-// 1.5 * 2^52 in the product's fma leaves the integer in the low bits.
+// the nearest integers to 127 y / s, where y and s are float64: see code_word.
 template <bool CODES, int TT, int NB, int R, int COLS, int WN>
 struct Rows {
     // a lane's values stay in registers between the halves if they are few
@@ -289,17 +312,42 @@ struct Rows {
                 });
             } else {
                 const double inv = zero ? 0.0 : 127.0 / top[tt];
-                double magic = 0x1.8p52;
+                double magic = kCodeMagic;
                 asm("" : "+v"(magic));  // a register: as a constant it is copied for every fma
                 static_for<0, NB>([&](auto b) {
-                    uint32_t q[R];
-                    static_for<0, R>([&](auto i) {
-                        double y;
-                        if constexpr (kKeep) y = y64[(tt * NB + b) * R + i];
-                        else y = scaled64(again(sum(tt, b, i)), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
-                        q[i] = (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(y, inv, magic));
+                    auto value = [&](int i) {
+                        if constexpr (kKeep) return y64[(tt * NB + b) * R + i];
+                        else return scaled64(again(sum(tt, b, i)), (double)as[tt], ws[chan(b) + i], bs[chan(b) + i]);
+                    };
+                    constexpr int kPart = R / 4 < 2 ? R / 4 : 2;  // words decided together: more would spill
+                    uint32_t w[R / 4];
+                    static_for<0, R / 4 / kPart>([&](auto part) {
+                        u16x2 least = {0xffff, 0xffff};  // the first: of the fractions
+                        static_for<part * kPart, (part + 1) * kPart>([&](auto c) {
+                            uint32_t q[4];
+                            static_for<0, 4>([&](auto e) {
+                                q[e] = code_word(value(c * 4 + e), inv, magic);
+                                least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, q[e]));
+                            });
+                            w[c] = pack_codes(q);
+                        });
+                        if (__builtin_expect(least[0] == 0, 0)) {
+                            double magic = kCodeMagic;  // formed again: words kept for this would spill too
+                            asm("" : "+v"(magic));
+                            static_for<part * kPart, (part + 1) * kPart>([&](auto c) {
+                                uint32_t q[4];
+                                static_for<0, 4>([&](auto e) {
+                                    const double y = value(c * 4 + e);
+                                    q[e] = code_word(y, inv, magic);
+                                    if ((q[e] & 0xffffu) == 0) q[e] = tie_word(q[e], y, top[tt]);
+                                    __builtin_amdgcn_sched_barrier(0);
+                                });
+                                w[c] = pack_codes(q);
+                            });
+                        }
                     });
-                    if (in) store_codes<R>(a.Y, t[tt], chan(b), a.N, q, zero);
+                    static_for<0, R / 4>([&](auto c) { w[c] = zero ? 0 : w[c]; });
+                    if (in) store_codes<R>(a.Y, t[tt], chan(b), a.N, w);
                     run_ends();
                 });
                 // codes * scale is y / ||y||, so scale = 1 / ||127 y / s||

@@ -1,6 +1,8 @@
 """Values at the ends of the float types on the GPU: NaN, infinities, the largest
 and smallest magnitudes, exact ties."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -186,3 +188,52 @@ def test_masked_rows_are_zeros_whatever_the_weights_hold(ms, T, d, K):
             codes, scale = ms.maxsim_embed_i8(a, s, w, ws2, b2, mask)
             assert not codes[out_of].any() and (scale[out_of] == 1).all()
             assert torch.isnan(scale[~out_of]).all()
+
+
+def _codes_of(y):
+    """The nearest integers to 127 y / max|y| of a row of float64, ties to even, in
+    rational arithmetic."""
+    exact = {v: Fraction(v) for v in set(y.tolist())}
+    top = max(abs(v) for v in exact.values())
+    code = {v: round(127 * f / top) if top else 0 for v, f in exact.items()}  # round(): half to even
+    return [code[v] for v in y.tolist()]
+
+
+def _products(acc, s, ws, b):
+    """float64 rows of sum * (a_scale * w_scale) + bias, rounded once (the scales'
+    product is exact in float64)."""
+    cache = {}
+
+    def one(a, x, w, c):
+        if (a, x, w, c) not in cache:
+            cache[a, x, w, c] = float(a * Fraction(x) * Fraction(w) + Fraction(c))
+        return cache[a, x, w, c]
+    return np.array([[one(int(a), x, w, c) for a, w, c in zip(row, ws, b)] for row, x in zip(acc, s)])
+
+
+@forms
+def test_embed_codes_at_ties(ms, T, d, K):
+    """Small sums under one weight scale put many channels on, and a tiny bias puts
+    them next to, the middle between two codes; the nearest code is taken there
+    too, and the even one on a tie."""
+    rng = np.random.default_rng(T + d + K)
+    a = np.zeros((T, K), np.int8)
+    for i in range(6):  # a few entries a row: sums of at most 24
+        a[np.arange(T), rng.integers(0, K, T)] = rng.integers(-2, 3, T)
+    w = rng.integers(-2, 3, (d, K)).astype(np.int8)
+    s = np.exp(rng.standard_normal(T)).astype(np.float32)
+    at = np.unique(np.concatenate([rng.integers(0, T, 60), [0, T - 1]]))
+    acc = a[at].astype(np.int64) @ w.T.astype(np.int64)
+    tiny = np.where(rng.random(d) < 0.5, 0.0, rng.choice([-1, 1], d) * 2.0 ** -rng.integers(28, 46, d)).astype(np.float32)
+    ties = 0
+    for scale, bias in ((0.37, None), (1.0, tiny)):
+        ws = np.full(d, scale, np.float32)
+        sc = s if bias is None else np.exp2(np.round(np.log2(s))).astype(np.float32)
+        dev = [torch.from_numpy(x).to(DEV) for x in (a, sc, w, ws)]
+        codes, _ = ms.maxsim_embed_i8(*dev, None if bias is None else torch.from_numpy(bias).to(DEV))
+        y = _products(acc, sc[at].tolist(), ws.tolist(), [0.0] * d if bias is None else bias.tolist())
+        want = np.array([_codes_of(row) for row in y])
+        top = np.abs(acc).max(1, keepdims=True)
+        ties += ((254 * acc) % np.maximum(2 * top, 1) == top).sum() if bias is None else 0
+        assert np.array_equal(codes.cpu().numpy()[at], want)
+    assert ties > 20
