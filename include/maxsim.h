@@ -61,7 +61,8 @@ typedef enum {
     MAXSIM_OK = 0,
     MAXSIM_ERR_NULL = 1,        /* a required pointer is NULL */
     MAXSIM_ERR_SHAPE = 2,       /* a negative size or inconsistent sizes */
-    MAXSIM_ERR_UNSUPPORTED = 3, /* a width or value out of range, an unknown dtype, a misaligned pointer */
+    MAXSIM_ERR_UNSUPPORTED = 3, /* d outside 1..1024 (rows of maxsim_embed.h: 1..131071), a value out of range,
+                                   an unknown dtype, a misaligned pointer */
     MAXSIM_ERR_OVERFLOW = 4,    /* an index or an int32 sum could overflow */
     MAXSIM_ERR_LAUNCH = 5       /* the HIP runtime refused a launch */
 } maxsim_status_t;

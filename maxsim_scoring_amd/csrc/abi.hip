@@ -566,7 +566,8 @@ const char* maxsim_status_string(maxsim_status_t s)
     case MAXSIM_OK: return "ok";
     case MAXSIM_ERR_NULL: return "a required pointer is NULL";
     case MAXSIM_ERR_SHAPE: return "negative or inconsistent sizes";
-    case MAXSIM_ERR_UNSUPPORTED: return "unsupported: a width or value out of range, an unknown dtype, or a misaligned pointer";
+    case MAXSIM_ERR_UNSUPPORTED: return "unsupported: a width (d outside 1..1024 in scoring and embeddings, rows outside 1..131071) or "
+                                       "value out of range, an unknown dtype, or a misaligned pointer";
     case MAXSIM_ERR_OVERFLOW: return "sizes overflow the int32 index range or the int32 sum";
     case MAXSIM_ERR_LAUNCH: return "kernel launch failed";
     default: return "unknown status";

@@ -172,3 +172,8 @@ def test_reference_generator_gives_the_published_values():
     assert ref.philox((ones,) * 4, (ones,) * 2) == [0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD]
     assert ref.philox((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0)) == [
         0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1]
+
+
+def test_status_text_names_the_widths(L):
+    text = L.maxsim_status_string(ERR_UNSUPPORTED).decode()
+    assert "1..1024" in text and "1..131071" in text
