@@ -237,3 +237,78 @@ def test_embed_codes_at_ties(ms, T, d, K):
         ties += ((254 * acc) % np.maximum(2 * top, 1) == top).sum() if bias is None else 0
         assert np.array_equal(codes.cpu().numpy()[at], want)
     assert ties > 20
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [1, 100, 128, 1030, 9001, 16640])
+def test_normalize_shows_nan_and_inf(ms, d, dtype):
+    """Rows with a NaN or an infinity are NaN, and so are their gradients; all
+    others are as without them."""
+    x, y, mask, bad = _spoiled(70, d, dtype, d + 1)
+    g = torch.randn(70, d, generator=torch.Generator(device=DEV).manual_seed(d), device=DEV)
+    u, rnorm = ms.maxsim_normalize_fwd(y, mask)
+    want, wnorm = ms.maxsim_normalize_fwd(x, mask)
+    # 1 / Inf is 0: only the row itself shows an infinity
+    assert torch.isnan(u[bad]).any(1).all() and not u[4].any() and rnorm[4] == 0
+    assert torch.equal(u[~bad], want[~bad]) and torch.equal(rnorm[~bad], wnorm[~bad])
+    dx = ms.maxsim_normalize_bwd(y, rnorm, g, out_dtype=torch.float32)
+    wx = ms.maxsim_normalize_bwd(x, wnorm, g, out_dtype=torch.float32)
+    assert torch.equal(dx[~bad], wx[~bad]) and torch.isnan(dx[bad]).any(1).all()
+
+
+def test_broken_states_reach_scores_and_top_k(ms):
+    """A document with a NaN state: the others' scores are those without it, and
+    the top-k's columns stay in range."""
+    Nq, Nd, Lq, Ld, K, d = 3, 40, 32, 50, 256, 128
+    g = torch.Generator(device=DEV).manual_seed(5)
+    hq = torch.randn(Nq, Lq, K, generator=g, device=DEV).bfloat16()
+    hd = torch.randn(Nd, Ld, K, generator=g, device=DEV).bfloat16()
+    _, _, w, ws, _ = _operands(1, d, K, 6)
+    eq, sq = ms.embed_tokens_i8(hq, w, ws)
+    want, _ = ms.maxsim_fwd_i8_tok(eq, sq, *ms.embed_tokens_i8(hd, w, ws))
+    hd[7, 3, 11] = float("nan")
+    hd[30] = float("inf")
+    ed, sd = ms.embed_tokens_i8(hd, w, ws)
+    assert torch.isnan(sd[7, 3]) and torch.isnan(sd[30]).all() and int(torch.isnan(sd).sum()) == 1 + Ld
+    scores, _ = ms.maxsim_fwd_i8_tok(eq, sq, ed, sd)
+    fine = torch.ones(Nd, dtype=torch.bool, device=DEV)
+    fine[[7, 30]] = False
+    assert torch.equal(scores[:, fine], want[:, fine])
+    idx, _, _ = ms.maxsim_topk(scores, Nd)
+    assert torch.equal(idx.long().sort(1).values, torch.arange(Nd, device=DEV).expand(Nq, Nd))
+    # a broken query token breaks that query alone
+    hq[1, 0, 0] = float("nan")
+    eq, sq = ms.embed_tokens_i8(hq, w, ws)
+    scores, _ = ms.maxsim_fwd_i8_tok(eq, sq, *ms.embed_tokens_i8(hd.nan_to_num(0, 0, 0), w, ws))
+    idx, _, _ = ms.maxsim_topk(scores, 10)
+    assert torch.isfinite(scores[[0, 2]]).all() and ((idx >= 0) & (idx < Nd)).all()
+
+
+@pytest.mark.parametrize("out", [torch.int8, torch.float16], ids=["i8", "fp16"])
+def test_captured_embeddings_spread_over_workgroups(ms, out):
+    """The form of three launches that keeps statistics in its output: two graphs of
+    it, replayed at once on streams of their own, against the eager calls."""
+    ops = [_operands(T, d, K, K) for T, d, K in ((32, 1024, 1024), (200, 272, 4096))]
+    graphs, outs = [], []
+    for o in ops:
+        ms.maxsim_embed_i8(*o, out_dtype=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ms.maxsim_embed_i8(*o, out_dtype=out))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in ops]
+    for r in range(4):
+        for a, s, *_ in ops:
+            a.neg_()
+            s.mul_(1.25)
+        want = [ms.maxsim_embed_i8(*o, out_dtype=out) for o in ops]
+        for g, s in zip(graphs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (e, s), (we, wsc) in zip(outs, want):
+            assert torch.equal(e, we) and (s is None or torch.equal(s, wsc))
