@@ -382,6 +382,29 @@ __device__ __forceinline__ void embed_rows(const LinearArgs& a, SUM sum, CHAN ch
 // Tiles through LDS
 // ---------------------------------------------------------------------------
 
+// Four dma_lds16 (NT: with the non-temporal hint) from one base to four KB in a
+// row of LDS; they share the wait states behind the base. Against four single
+// loads, 200,000 x 2048 to 256 channels take 167.7 instead of 181.3 us and
+// 8192 x 4096 x 4096 125.0 instead of 127.0.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+#define MAXSIM_DMA4(HINT)                                                                                    \
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %5" HINT                       \
+                 "\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %5" HINT            \
+                 "\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %5" HINT            \
+                 "\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %5" HINT            \
+                 :                                                                                           \
+                 : "s"(lds), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(base)               \
+                 : "memory", "m0", "scc")
+template <bool NT>
+__device__ __forceinline__ void dma_lds16_x4(const void* base, const uint32_t* voff, uint32_t lds)
+{
+    if constexpr (NT) MAXSIM_DMA4(" nt");
+    else MAXSIM_DMA4("");
+}
+#undef MAXSIM_DMA4
+#pragma clang diagnostic pop
+
 // position of 16-byte chunk c of a row of KB bytes, against bank conflicts
 template <int KB>
 __device__ __forceinline__ int place(int row, int c)
@@ -584,10 +607,16 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
             const int8_t* pa = A + (int64_t)ki * KB;
             const int8_t* pw = W + (int64_t)ki * KB;
             const uint32_t at = ring0 + (uint32_t)(i % ST) * C::kStage;
+            constexpr int kGroup = C::kPerWave % 4 == 0 && C::kLoads % C::kWaves == 0 && BT % (4 * C::kRows) == 0 ? 4 : 1;
 #pragma unroll
-            for (int j = 0; j < C::kPerWave; ++j) {
+            for (int j = 0; j < C::kPerWave; j += kGroup) {
                 const int base = row_of(j);
                 const uint32_t to = (uint32_t)uniform((int)(at + base * KB));
+                if constexpr (kGroup == 4) {
+                    if (EMBED && base < BT) dma_lds16_x4<true>(uniform_ptr(pa), &voff[j], to);
+                    else dma_lds16_x4<false>(uniform_ptr(base < BT ? pa : pw), &voff[j], to);
+                    continue;
+                }
                 // embeddings: the hidden states pass once, W is read by every workgroup
                 if (EMBED && base < BT) dma_lds16_nt(uniform_ptr(pa), voff[j], to);
                 else if (C::kLoads % C::kWaves == 0 || base < BT + BN)
