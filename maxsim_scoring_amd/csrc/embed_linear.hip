@@ -11,13 +11,13 @@
 //
 // stream_kernel: embeddings of up to 256 channels, K up to 1024. The weights stay
 // in registers and the hidden states pass once, so memory bounds it: 360,000 x 768
-// states to 128 codes take 71 us, 4.5 TB/s of states and codes, against 60 us for
-// a copy of as many bytes.
+// states to 128 codes take 72 to 77 us (by card), 4.2 to 4.5 TB/s of states and
+// codes, against 60 us for a copy of as many bytes.
 // tile_kernel: BT tokens x BN channels per workgroup; A and W tiles of KB bytes
 // along k stream through a ring in LDS by direct-to-LDS loads, with 16-byte
 // chunks swizzled against bank conflicts. Large products are bound by the matrix
-// cores and their power: 8192 x 4096 x 4096 in 120 us, 2.29 POP/s (an MFMA-only
-// loop on such data reaches 3.4).
+// cores and their power: 8192 x 4096 x 4096 in 118 to 125 us (by card), 2.2 to 2.3
+// POP/s (an MFMA-only loop on such data reaches 3.4).
 // few_kernel: a few tokens. W is the traffic; every fragment goes straight from
 // memory to registers, waves split k, and LDS joins their sums. One token through
 // 4096 x 4096 weights takes 5.3 us, 2.8 of them the launch. With join_kernel it
@@ -600,7 +600,7 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_kernel(LinearArgs a)
         // The order of k does not matter to whole numbers. Rows a multiple of 4 KB
         // apart meet the same few memory channels at one k, so workgroups that read
         // their hidden states from memory start at different ones (100,000 x 4096 to
-        // 128 channels 108 us, 121 without).
+        // 128 channels 102 us, 121 without).
         const int first = EMBED && (a.K & 4095) == 0 ? (int)(blockIdx.x % (unsigned)nk) : 0;
         auto issue = [&](int i) {
             const int ki = first + i < nk ? first + i : first + i - nk;
@@ -795,7 +795,7 @@ __global__ __launch_bounds__(NWV * 64, 2) void stream_kernel(LinearArgs a)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
             acc = mfma32<kI8>(w[s], *(const i32x4*)(st + off[s & 7] + (s >> 3) * 256), acc);
-        // the next loads follow the MFMAs (72 us for the 360,000 x 768 states, 78
+        // the next loads follow the MFMAs (73 us for the 360,000 x 768 states, 81
         // with the loads in front of them)
         if (i + ST - 1 < count) issue(i + ST - 1);
         finish(i + 1);
@@ -1032,12 +1032,12 @@ void run_few(const LinearArgs& a, hipStream_t stream)
 
 // Tiles by how many the launch has (median us of N = K = 4096 bf16 outputs with
 // 256 x 256 / 128 x 128 / 64 x 128 / 64 x 64 tiles):
-//   T = 8192  122 / 134 / 167 / 207     2048   49 /  36 /  44 /  52
-//   T = 4096   62 /  68 /  85 / 100     1024   47 /  26 /  24 /  28
-//   T =  512   47 /  24 /  18 /  16       96   44 /  23 /  17 /  11
+//   T = 8192  117 / 132 / 168 / 208     2048   48 /  36 /  44 /  52
+//   T = 4096   61 /  68 /  84 / 101     1024   48 /  25 /  23 /  28
+//   T =  512   46 /  23 /  17 /  16       96   43 /  23 /  16 /  12
 // One 256 x 256 tile fills a CU, two or more of the smaller ones share it. Up to
-// 32 tokens the direct form is ahead (32 tokens 8.7 against 10.8 us, 16 6.5
-// against 10.8; 64 tokens 13.1 against 11.0).
+// 32 tokens the direct form is ahead (32 tokens 8.8 against 11.1 us, 16 6.6
+// against 11.1; 64 tokens 14.2 against 11.2).
 template <bool UNAL>
 void linear_tiles(const LinearArgs& a, hipStream_t stream)
 {
@@ -1059,8 +1059,8 @@ void linear_once(const LinearArgs& a, hipStream_t stream)
 
 // Every workgroup holds whole rows, so the tile's tokens shrink as the channels
 // grow. Up to 128 channels two workgroups of 128 tokens share a CU: 200,000 tokens
-// of 2048 to 128 channels take 115 us, 127 with one of 256 tokens, 149 with
-// 64-byte steps of k; to 256 channels 169 us with 256 tokens, 192 with 128.
+// of 2048 to 128 channels take 111 us, 129 with one of 256 tokens, 145 with
+// 64-byte steps of k; to 256 channels 156 us with 256 tokens, 193 with 128.
 template <bool UNAL>
 void embed_tiles(const LinearArgs& a, hipStream_t stream)
 {
@@ -1103,13 +1103,13 @@ void embed_stream(const LinearArgs& a, hipStream_t stream)
 // has a workgroup: the first launch leaves the tile's statistics of each row in the
 // 16 bytes or more of E that the tile will fill, the second joins a row's, the
 // third forms the sums again (W comes from the caches then) and overwrites its own
-// place. 32 tokens of 1024 to 1024 channels take 10.6 us, 23.7 in tiles of whole
-// rows; of 4096 to 128 17.8 us, 30.9 in the direct form. Three launches cost about
+// place. 32 tokens of 1024 to 1024 channels take 10.5 us, 27.5 in tiles of whole
+// rows; of 4096 to 128 17.6 us, 30.9 in the direct form. Three launches cost about
 // 5 us more than one, so it takes over 160,000 weights to pay (1000 to 128 channels
-// 10.6 against 7.2 us, 1536 to 128 11.3 against 13.6), beyond 256 channels, where
-// the other choice is tiles, any number (64 to 512 channels 8.3 against 7.7 us, to
-// 1024 8.5 against 11.0). From 1024 tokens on the tiles are ahead (768 to 768
-// channels 17.7 against 23.2 us; 512 tokens 17.4 against 15.3).
+// 10.7 against 7.2 us, 1536 to 128 11.2 against 13.6), beyond 256 channels, where
+// the other choice is tiles, any number (64 to 512 channels 8.5 against 8.6 us, to
+// 1024 8.6 against 13.7). From 1024 tokens on the tiles are ahead (768 to 768
+// channels 20.0 against 22.4 us; 512 tokens 19.5 against 14.8).
 constexpr int64_t kSplitTokens = 512, kSplitWeights = 160000;
 bool split_ok(const LinearArgs& a)
 {
@@ -1124,11 +1124,12 @@ void embed_split(const LinearArgs& a, hipStream_t stream)
     else run_few<2, 1, 1, 8, kFinish>(a, stream);
 }
 
-// The streamed form where it fits, at any number of tokens (1 to 4096 tokens of
-// 768 to 128 channels 6.0 to 7.1 us; direct form 8.7 to 9.2, tiles 12.7 to 14.1).
-// Elsewhere few tokens spread their channels over workgroups if the weights are
-// many, or take the direct form up to 256 channels (4096 tokens of 2048 to 128
-// channels 18.3 us, tiles 27.8), and tiles beyond.
+// The streamed form where it fits, at any number of tokens (32 to 4096 tokens of
+// 768 to 128 channels 6.4 to 7.1 us, direct form 8.5 to 9.1, tiles 8.9 to 11.8; a
+// single token 6.4 in both the first). Elsewhere few tokens spread their channels
+// over workgroups if the weights are many, or take the direct form up to 256
+// channels (4096 tokens of 2048 to 128 channels 18.0 us, tiles 20.5; 1024 tokens
+// 17.4, tiles 15.2), and tiles beyond.
 void embed_once(const LinearArgs& a, hipStream_t stream)
 {
     if (stream_ok(a)) return embed_stream(a, stream);

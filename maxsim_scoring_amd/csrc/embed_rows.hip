@@ -7,8 +7,11 @@
 // waves and a reduction takes log2(G) cross-lane steps; each lane holds VPL
 // chunks of VB bytes. Rows too long for that are read twice (the second time
 // from the L2). Measured: codes of 360,000 x 128 fp16 rows, a quarter of them
-// masked, in 21.4 to 23.9 us (4.9 to 5.4 TB/s; a copy reaches 5.4), 131,072 x 128
+// masked, in 21.4 to 23.6 us (5.0 to 5.5 TB/s; a copy reaches 5.4), 131,072 x 128
 // bf16 rows normalised in 11.0 us (5.4 TB/s), their gradient in 23.3 (5.8 TB/s).
+// Rows that 16 bytes do not divide go element by element: 131,072 rows of 100 bf16
+// values take 27 us to codes, 27 normalised, 35 in the gradient; of 128 values
+// 11.7, 11.9 and 23.4.
 #include "embed_common.hpp"
 #include "kernels.hpp"
 
@@ -572,10 +575,10 @@ unsigned row_blocks(int64_t T, int rows)
 // Picks the lanes per row and chunks per lane from the number of chunks; V
 // chunks per lane in the narrow classes. Quantisation's work per row (its
 // reduction, reciprocal and scale) is as long as that of a chunk, so two chunks
-// share it: 360,000 rows of 128 fp16 values take 21.4 us with 8 lanes x 2 chunks,
-// 42.4 with 16 x 1 and 23.7 with 4 x 4; normalisation of 131,072 such rows 11.0,
-// 11.4 and 11.0 us; its gradient, with 48 bytes to load per chunk, 23.7, 23.1
-// and 24.4 us.
+// share it: 360,000 rows of 128 fp16 values take 21.5 us with 8 lanes x 2 chunks,
+// 43 with 16 x 1 and 23.7 with 4 x 4; normalisation of 131,072 such rows 10.9,
+// 11.3 and 10.9 us; its gradient, with 48 bytes to load per chunk, 23.8, 23.0
+// and 24.2 us.
 #define MAXSIM_ROWS(KERNEL, LONG, E, VB, V, MAXV)                                                            \
     do {                                                                                                     \
         const int nv = a.d / (VB / elem_bytes<E>());                                                          \
