@@ -71,6 +71,20 @@ def lib() -> ctypes.CDLL:
         L.maxsim_normalize_bwd.argtypes = [ci, vp, vp, vp, i64, i64, ci, vp, vp]
         L.maxsim_dropout_fwd.argtypes = [ci, vp, i64, f64, u64, u64, vp, vp, vp]
         L.maxsim_dropout_bwd.argtypes = [ci, vp, i64, f64, u64, u64, vp, vp, vp]
+        L.maxsim_quantize_mx4.argtypes = [ci, vp, i64, i64, vp, ci, vp, vp, vp]
+        L.maxsim_dequantize_mx4.argtypes = [vp, vp, i64, i64, ci, vp, vp]
+        L.maxsim_linear_mx4.argtypes = [ci, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp]
+        L.maxsim_fwd_mx4.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.maxsim_logprob_workspace.argtypes = [i64, i64, i64, i64]
+        L.maxsim_logprob_workspace.restype = i64
+        L.maxsim_logprob_fwd.argtypes = [ci, vp, i64, i64, f32, vp, vp, i64, i64, vp, vp, vp, vp, vp,
+                                         vp, vp, i64, vp]
+        L.maxsim_logprob_bwd.argtypes = [ci, vp, i64, i64, f32, vp, vp, i64, vp, vp, vp, vp, ci, vp,
+                                         vp]
+        L.maxsim_logprob_fwd.restype = L.maxsim_logprob_bwd.restype = ci
+        for f in (L.maxsim_quantize_mx4, L.maxsim_dequantize_mx4, L.maxsim_linear_mx4,
+                  L.maxsim_fwd_mx4):
+            f.restype = ci
         for f in (L.maxsim_quantize_tok, L.maxsim_linear_i8, L.maxsim_embed_i8,
                   L.maxsim_normalize_fwd, L.maxsim_normalize_bwd, L.maxsim_dropout_fwd,
                   L.maxsim_dropout_bwd):
@@ -808,3 +822,270 @@ def maxsim_dropout_bwd(dY: torch.Tensor, p: float, seed: int, step: int = 0,
                        stream=None):
     """Gradient of maxsim_dropout_fwd with the same p, seed and step. Returns dX."""
     return _dropout("maxsim_dropout_bwd", dY, p, seed, step, step_dev, dX, stream, ("dY", "dX"))
+
+
+# ---------------------------------------------------------------------------
+# 4-bit embeddings (include/maxsim_mx4.h): a row of d values is uint8 codes
+# [..., 16 B], two in a byte, and uint8 scales [..., B], B = ceil(d / 32).
+# ---------------------------------------------------------------------------
+
+def _mx4_rows(name: str, codes: torch.Tensor, scale: torch.Tensor, d: Optional[int]):
+    """(leading shape, rows, width, blocks) of 4-bit rows. Without d the width is
+    that of whole blocks."""
+    if codes.dtype != torch.uint8 or scale.dtype != torch.uint8:
+        raise ValueError(f"{name} and its scale must be uint8")
+    if scale.dim() < 1 or codes.dim() != scale.dim():
+        raise ValueError(f"{name} must be [..., 16 B] and its scale [..., B]")
+    lead, B = scale.shape[:-1], scale.shape[-1]
+    if codes.shape != lead + (16 * B,):
+        raise ValueError(f"{name} must have shape {list(lead) + [16 * B]}, got {list(codes.shape)}")
+    if d is None:
+        d = 32 * B
+    elif (int(d) + 31) // 32 != B:
+        raise ValueError(f"{name} has {B} blocks of 32 in a row, not those of d = {d}")
+    return lead, math.prod(lead), int(d), B
+
+
+def maxsim_quantize_mx4(X: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                        normalize: bool = False, codes: Optional[torch.Tensor] = None,
+                        scale: Optional[torch.Tensor] = None, stream=None):
+    """Rows X [..., d] fp16/bf16/fp32 (with ``normalize`` over their norms) to
+    4-bit codes and one power of two for each 32 of them. mask uint8 [...]: masked
+    rows give codes 0, scales 127 (2^0). Returns (codes uint8 [..., 16 B], scale
+    uint8 [..., B])."""
+    code = _row_type("X", X.dtype)
+    shape, lead, T, d = _rows("X", X)
+    B = (d + 31) // 32
+    _has("mask", mask, torch.uint8, lead)
+    _has("codes", codes, torch.uint8, lead + (16 * B,))
+    _has("scale", scale, torch.uint8, lead + (B,))
+    index = _place("X mask codes scale", X, mask, codes, scale)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_quantize_mx4(X, mask, normalize, codes, scale)
+    if codes is None:
+        codes = torch.empty(lead + (16 * B,), dtype=torch.uint8, device=X.device)
+    if scale is None:
+        scale = torch.empty(lead + (B,), dtype=torch.uint8, device=X.device)
+    _check("maxsim_quantize_mx4",
+           lib().maxsim_quantize_mx4(code, X.data_ptr(), T, d, _at(mask), bool(normalize),
+                                     codes.data_ptr(), scale.data_ptr(), _raw_stream(index)))
+    return codes, scale
+
+
+def maxsim_dequantize_mx4(codes: torch.Tensor, scale: torch.Tensor, d: Optional[int] = None,
+                          out_dtype=torch.bfloat16, Y: Optional[torch.Tensor] = None, stream=None):
+    """The values of 4-bit rows: codes [..., 16 B], scale [..., B] to Y [..., d] of
+    ``out_dtype`` (fp16, bf16 or fp32); d is 32 B by default."""
+    lead, T, d, _ = _mx4_rows("codes", codes, scale, d)
+    dt = out_dtype if Y is None else Y.dtype
+    code = _row_type("out_dtype", dt)
+    _has("Y", Y, dt, lead + (d,))
+    index = _place("codes scale Y", codes, scale, Y)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_dequantize_mx4(codes, scale, d, dt, Y)
+    if Y is None:
+        Y = torch.empty(lead + (d,), dtype=dt, device=codes.device)
+    _check("maxsim_dequantize_mx4",
+           lib().maxsim_dequantize_mx4(codes.data_ptr(), scale.data_ptr(), T, d, code,
+                                       Y.data_ptr(), _raw_stream(index)))
+    return Y
+
+
+def maxsim_linear_mx4(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor,
+                      w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                      out_dtype=torch.bfloat16, Y: Optional[torch.Tensor] = None, stream=None):
+    """Product A W^T + bias of 4-bit rows. A [..., 16 B] with a_scale [..., B], W
+    [N, 16 B] with w_scale [N, B], bias float32 [N]. Returns Y [..., N] of
+    ``out_dtype`` (fp16, bf16 or fp32)."""
+    lead, T, K, B = _mx4_rows("A", A, a_scale, None)
+    wlead, N, _, wB = _mx4_rows("W", W, w_scale, None)
+    if len(wlead) != 1 or wB != B:
+        raise ValueError(f"W must be [N, {16 * B}], got {list(W.shape)}")
+    _has("bias", bias, torch.float32, (N,))
+    dt = out_dtype if Y is None else Y.dtype
+    code = _row_type("out_dtype", dt)
+    _has("Y", Y, dt, lead + (N,))
+    index = _place("A a_scale W w_scale bias Y", A, a_scale, W, w_scale, bias, Y)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_linear_mx4(A, a_scale, W, w_scale, bias, dt, Y)
+    if Y is None:
+        Y = torch.empty(lead + (N,), dtype=dt, device=A.device)
+    _check("maxsim_linear_mx4",
+           lib().maxsim_linear_mx4(code, A.data_ptr(), a_scale.data_ptr(), W.data_ptr(),
+                                   w_scale.data_ptr(), _at(bias), T, N, K, Y.data_ptr(),
+                                   _raw_stream(index)))
+    return Y
+
+
+def maxsim_fwd_mx4(Q: torch.Tensor, q_scale: torch.Tensor, D: torch.Tensor, d_scale: torch.Tensor,
+                   q_mask: Optional[torch.Tensor] = None, d_mask: Optional[torch.Tensor] = None,
+                   want_argmax: bool = False, scores: Optional[torch.Tensor] = None,
+                   argmax: Optional[torch.Tensor] = None, stream=None):
+    """MaxSim of 4-bit token embeddings: Q [Nq,Lq,16 B], q_scale [Nq,Lq,B],
+    D [Nd,Ld,16 B], d_scale [Nd,Ld,B] uint8; masks uint8. Returns (scores float32
+    [Nq,Nd], argmax int32 [Nq,Nd,Lq] or None)."""
+    qlead, _, d, B = _mx4_rows("Q", Q, q_scale, None)
+    dlead, _, _, dB = _mx4_rows("D", D, d_scale, None)
+    if len(qlead) != 2 or len(dlead) != 2 or dB != B:
+        raise ValueError("Q and D must be [N, L, 16 B] with the same number of blocks")
+    (Nq, Lq), (Nd, Ld) = qlead, dlead
+    _has("q_mask", q_mask, torch.uint8, qlead)
+    _has("d_mask", d_mask, torch.uint8, dlead)
+    _has("scores", scores, torch.float32, (Nq, Nd))
+    _has("argmax", argmax, torch.int32, (Nq, Nd, Lq))
+    index = _place("Q q_scale D d_scale q_mask d_mask scores argmax", Q, q_scale, D, d_scale, q_mask,
+                   d_mask, scores, argmax)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_fwd_mx4(Q, q_scale, D, d_scale, q_mask, d_mask, want_argmax, scores, argmax)
+    if scores is None:
+        scores = torch.empty((Nq, Nd), dtype=torch.float32, device=Q.device)
+    if argmax is None and want_argmax:
+        argmax = torch.empty((Nq, Nd, Lq), dtype=torch.int32, device=Q.device)
+    _check("maxsim_fwd_mx4",
+           lib().maxsim_fwd_mx4(Q.data_ptr(), q_scale.data_ptr(), D.data_ptr(), d_scale.data_ptr(),
+                                Nq, Nd, Lq, Ld, d, _at(q_mask), _at(d_mask), scores.data_ptr(),
+                                _at(argmax), _raw_stream(index)))
+    return scores, argmax
+
+
+def embed_tokens_mx4(H: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                     stream=None):
+    """Hidden states H [..., K] fp16/bf16/fp32 to 4-bit token embeddings through a
+    4-bit projection (W [d, 16 B], w_scale [d, B]): the states are quantised,
+    multiplied, normalised and quantised again. Three library calls. Returns
+    (codes, scale) as maxsim_quantize_mx4, masked rows as there."""
+    a, a_scale = maxsim_quantize_mx4(H, mask, stream=stream)
+    y = maxsim_linear_mx4(a, a_scale, W, w_scale, bias, out_dtype=torch.float32, stream=stream)
+    return maxsim_quantize_mx4(y, mask, normalize=True, stream=stream)
+
+
+def two_stage_topk_mx4(Qm: torch.Tensor, q_scale: torch.Tensor, Dm: torch.Tensor,
+                       d_scale: torch.Tensor, Qf: torch.Tensor, Df: torch.Tensor, k: int,
+                       candidates: int, q_mask: Optional[torch.Tensor] = None,
+                       d_mask: Optional[torch.Tensor] = None, stream=None):
+    """two_stage_topk with a 4-bit scan: maxsim_fwd_mx4 scores of every doc, the
+    `candidates` best docs per query, exact fp16/bf16 scores of those (query, doc)
+    pairs, and the top-k of the rescored candidates. Four library calls. Returns
+    (doc idx int32 [Nq,k], exact scores float32 [Nq,k], scan scores [Nq,Nd])."""
+    Nq = Qm.shape[0]
+    scan, _ = maxsim_fwd_mx4(Qm, q_scale, Dm, d_scale, q_mask, d_mask, stream=stream)
+    cand, _, cand_q = maxsim_topk(scan, candidates, want_rows=True, stream=stream)
+    exact, _ = maxsim_fwd_pairs(Qf, Df, cand_q.view(-1), cand.view(-1), q_mask, d_mask,
+                                stream=stream)
+    doc, val, _ = maxsim_topk(exact.view(Nq, candidates), k, ids=cand, stream=stream)
+    return doc, val, scan
+
+
+# ---------------------------------------------------------------------------
+# Log probabilities of columns of a score matrix (include/maxsim_loss.h)
+# ---------------------------------------------------------------------------
+
+def _logprob_args(X, targets, mask):
+    if X.dim() != 2 or targets.dim() != 2 or targets.shape[0] != X.shape[0]:
+        raise ValueError("X must be [Nq, Nd] and targets [Nq, P]")
+    code = _row_type("X", X.dtype)
+    if targets.dtype != torch.int32:
+        raise ValueError(f"targets must be int32, got {targets.dtype}")
+    _has("mask", mask, torch.uint8, X.shape)
+    return code, X.shape[0], X.shape[1], targets.shape[1]
+
+
+def maxsim_logprob_fwd(X: torch.Tensor, targets: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                       scale: float = 1.0, k: int = 0, logp: Optional[torch.Tensor] = None,
+                       rank: Optional[torch.Tensor] = None, norm: Optional[torch.Tensor] = None,
+                       entropy: Optional[torch.Tensor] = None,
+                       top_idx: Optional[torch.Tensor] = None,
+                       top_logp: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Log probabilities of columns ``targets`` [Nq, P] int32 under the softmax of
+    ``scale`` X, rows of scores X [Nq, Nd] (fp16/bf16/fp32), mask uint8 [Nq, Nd].
+    Returns (logp [Nq, P], rank int32 [Nq, P], norm [Nq, 2], entropy [Nq],
+    top_idx int32 [Nq, k], top_logp [Nq, k]; the last two None with k = 0).
+    ``workspace`` is uint8 of maxsim_logprob_workspace bytes."""
+    code, Nq, Nd, P = _logprob_args(X, targets, mask)
+    k = int(k)
+    if not 0 <= k <= 1024:
+        raise ValueError(f"k must be in [0, 1024], got {k}")
+    _has("logp", logp, torch.float32, (Nq, P))
+    _has("rank", rank, torch.int32, (Nq, P))
+    _has("norm", norm, torch.float32, (Nq, 2))
+    _has("entropy", entropy, torch.float32, (Nq,))
+    _has("top_idx", top_idx, torch.int32, (Nq, k))
+    _has("top_logp", top_logp, torch.float32, (Nq, k))
+    need = lib().maxsim_logprob_workspace(Nq, Nd, P, k)
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.numel() < need):
+        raise ValueError(f"workspace must be uint8 of at least {need} bytes")
+    index = _place("X targets mask logp rank norm entropy top_idx top_logp workspace", X, targets, mask,
+                   logp, rank, norm, entropy, top_idx, top_logp, workspace)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_logprob_fwd(X, targets, mask, scale, k, logp, rank, norm, entropy, top_idx,
+                                      top_logp, workspace)
+    dev = X.device
+    if logp is None:
+        logp = torch.empty((Nq, P), dtype=torch.float32, device=dev)
+    if rank is None:
+        rank = torch.empty((Nq, P), dtype=torch.int32, device=dev)
+    if norm is None:
+        norm = torch.empty((Nq, 2), dtype=torch.float32, device=dev)
+    if entropy is None:
+        entropy = torch.empty((Nq,), dtype=torch.float32, device=dev)
+    if k and top_idx is None:
+        top_idx = torch.empty((Nq, k), dtype=torch.int32, device=dev)
+    if k and top_logp is None:
+        top_logp = torch.empty((Nq, k), dtype=torch.float32, device=dev)
+    if workspace is None and need > 0:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _check("maxsim_logprob_fwd",
+           lib().maxsim_logprob_fwd(code, X.data_ptr(), Nq, Nd, float(scale), _at(mask),
+                                    targets.data_ptr(), P, k, logp.data_ptr(), rank.data_ptr(),
+                                    norm.data_ptr(), entropy.data_ptr(), _at(top_idx),
+                                    _at(top_logp), _at(workspace),
+                                    0 if workspace is None else workspace.numel(),
+                                    _raw_stream(index)))
+    return logp, rank, norm, entropy, top_idx, top_logp
+
+
+def maxsim_logprob_bwd(X: torch.Tensor, targets: torch.Tensor, norm: torch.Tensor,
+                       grad_logp: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                       scale: float = 1.0, entropy: Optional[torch.Tensor] = None,
+                       grad_entropy: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                       dX: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of maxsim_logprob_fwd with respect to X, from its norm (and, with
+    grad_entropy [Nq], its entropy): grad_logp float32 [Nq, P]. Returns dX [Nq, Nd]
+    of ``out_dtype``; in float32 it is the grad_scores of maxsim_bwd."""
+    code, Nq, Nd, P = _logprob_args(X, targets, mask)
+    _has("norm", norm, torch.float32, (Nq, 2))
+    _has("grad_logp", grad_logp, torch.float32, (Nq, P))
+    if (entropy is None) != (grad_entropy is None):
+        raise ValueError("entropy and grad_entropy go together")
+    _has("entropy", entropy, torch.float32, (Nq,))
+    _has("grad_entropy", grad_entropy, torch.float32, (Nq,))
+    dt = out_dtype if dX is None else dX.dtype
+    xt = _row_type("out_dtype", dt)
+    _has("dX", dX, dt, X.shape)
+    index = _place("X targets norm grad_logp mask entropy grad_entropy dX", X, targets, norm, grad_logp,
+                   mask, entropy, grad_entropy, dX)
+    there = _elsewhere(stream, index)
+    if there is not None:
+        with there:
+            return maxsim_logprob_bwd(X, targets, norm, grad_logp, mask, scale, entropy, grad_entropy,
+                                      dt, dX)
+    if dX is None:
+        dX = torch.empty_like(X, dtype=dt)
+    _check("maxsim_logprob_bwd",
+           lib().maxsim_logprob_bwd(code, X.data_ptr(), Nq, Nd, float(scale), _at(mask),
+                                    targets.data_ptr(), P, norm.data_ptr(), _at(entropy),
+                                    grad_logp.data_ptr(), _at(grad_entropy), xt, dX.data_ptr(),
+                                    _raw_stream(index)))
+    return dX

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmaxsim_amd.so")
 SOURCES = ["abi.hip", "fwd_dense.hip", "fwd_varlen.hip", "fwd_dim.hip", "bwd.hip", "topk.hip", "chamfer.hip",
-           "embed_abi.hip", "embed_rows.hip", "embed_linear.hip"]
+           "embed_abi.hip", "embed_rows.hip", "embed_linear.hip",
+           "mx4_abi.hip", "mx4_rows.hip", "mx4_linear.hip", "fwd_mx4.hip", "logprob_abi.hip", "logprob.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -37,11 +38,13 @@ FLAGS = [
 # accumulation registers (no copy back per MFMA); the other kernels keep the
 # compiler's default register form. The embedding head carries activations and
 # gradients, where an overflow upstream must stay visible: NaNs are honoured
-# there (later flags win). They are in the top-k too, which keeps k candidates
+# there (later flags win), as they are where 4-bit rows mark a NaN by their scale,
+# and in the top-k, which keeps k candidates
 # whatever the scores hold.
 _NANS = ["-Xarch_device", "-fhonor-nans", "-Xarch_device", "-mamdgpu-ieee"]
 EXTRA = {"chamfer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "topk.hip": _NANS, "embed_rows.hip": _NANS, "embed_linear.hip": _NANS}
+         "topk.hip": _NANS, "embed_rows.hip": _NANS, "embed_linear.hip": _NANS,
+         "mx4_rows.hip": _NANS, "mx4_linear.hip": _NANS, "fwd_mx4.hip": _NANS, "logprob.hip": _NANS}
 
 
 def _run(cmd, verbose):

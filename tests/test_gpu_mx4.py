@@ -1,0 +1,504 @@
+"""4-bit rows on the GPU against plain float64 forms (mx4_reference.py, which
+also derives the bounds). Codes and scales are compared exactly."""
+
+import numpy as np
+import pytest
+import torch
+
+import mx4_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+short = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
+by_type = pytest.mark.parametrize("dtype", TYPES, ids=short.get)
+
+
+@pytest.fixture(scope="module")
+def ms():
+    import maxsim_scoring_amd as m
+    m.binding.lib()
+    assert torch.cuda.is_available()
+    return m
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _rows(T, d, dtype, seed):
+    g = _gen(seed)
+    x = torch.randn(T, d, generator=g, device=DEV) * torch.exp(torch.randn(T, d, generator=g, device=DEV))
+    return x.to(dtype)
+
+
+def _mask(shape, seed, keep=0.7):
+    return (torch.rand(shape, generator=_gen(seed), device=DEV) < keep).to(torch.uint8)
+
+
+def _guarded(shape, dtype, fill):
+    """A tensor with a guard behind it: (tensor, check of the guard)."""
+    n = int(np.prod(shape))
+    buf = torch.full((n + 256,), fill, dtype=dtype, device=DEV)
+    return buf[:n].view(shape), lambda: bool((buf[n:] == fill).all())
+
+
+def _off_by_one(t):
+    """The same values at an odd address."""
+    buf = torch.empty(t.numel() + 1, dtype=torch.uint8, device=t.device)
+    buf[1:] = t.reshape(-1)
+    return buf[1:].view(t.shape)
+
+
+def _random_mx4(lead, d, seed, spread=4):
+    """Codes of every value and scales of a few neighbouring exponents; zeros behind d."""
+    g = _gen(seed)
+    B = ref.blocks(d)
+    n = torch.randint(0, 16, (*lead, B * 32), generator=g, device=DEV, dtype=torch.int32)
+    n[..., d:] = 0
+    codes = (n[..., 0::2] | n[..., 1::2] << 4).to(torch.uint8)
+    scale = torch.randint(120, 120 + spread, (*lead, B), generator=g, device=DEV).to(torch.uint8)
+    return codes, scale
+
+
+def _values(codes, scale):
+    """Float64 on the GPU."""
+    lead = scale.shape[:-1]
+    v = ref.values(codes.reshape(-1, codes.shape[-1]).cpu().numpy(), scale.reshape(-1, scale.shape[-1]).cpu().numpy())
+    return torch.from_numpy(v).to(DEV).view(*lead, -1)
+
+
+# ------------------------------------------------------------- rows
+
+ROWS = [(1, 1), (3, 7), (5, 31), (5, 32), (37, 33), (64, 64), (33, 100), (1000, 128), (17, 200), (9, 516), (32, 768),
+        (7, 1000), (3, 1030), (5, 2050), (4, 4096), (3, 8192), (2, 9001), (2, 16640), (1, 131071)]
+
+
+def _check_codes(got, want):
+    codes, scale = got
+    wcode, wscale = want
+    assert np.array_equal(scale.cpu().numpy(), wscale)
+    n = codes.cpu().numpy()
+    n = np.stack([n & 15, n >> 4], -1).reshape(n.shape[0], -1)
+    # a zero's sign is free where the value is not a negative zero itself
+    differ = (n != wcode) & ~((n % 8 == 0) & (wcode % 8 == 0))
+    assert not differ.any(), f"{differ.sum()} codes differ, first at {np.argwhere(differ)[0]}"
+
+
+@by_type
+@pytest.mark.parametrize("T,d", ROWS)
+def test_quantize(ms, T, d, dtype):
+    x = _rows(T, d, dtype, T + d)
+    B = ref.blocks(d)
+    for normalize in (False, True):
+        for mask in (None, _mask((T,), d)):
+            codes, ok1 = _guarded((T, 16 * B), torch.uint8, 0xA5)
+            scale, ok2 = _guarded((T, B), torch.uint8, 0xA5)
+            ms.maxsim_quantize_mx4(x, mask, normalize=normalize, codes=codes, scale=scale)
+            torch.cuda.synchronize()
+            assert ok1() and ok2()
+            _check_codes((codes, scale), ref.quantize(x.double().cpu().numpy(), None if mask is None else mask.cpu().numpy(),
+                                                      normalize))
+
+
+def test_quantize_borders(ms):
+    """Every border between levels, the values next to it, and the powers of two, at exponents over the whole range."""
+    base = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.999999, 0.5, 1, 2, 3, 4, 0.0], dtype=np.float32)
+    near = np.concatenate([base, np.nextafter(base, np.float32(9)), np.nextafter(base, np.float32(-9)), -base])
+    rows = []
+    for e in (0, 1, -1, 30, -30, 100, -100, 124, -120, -125, -126, -130, -140):
+        for top in (4.0, 7.0, 6.0):
+            for at in range(0, len(near), 31):
+                row = np.zeros(32, dtype=np.float32)
+                part = near[at:at + 31]
+                row[:len(part)] = part
+                row[31] = top
+                rows.append(np.ldexp(row, e))
+    x = torch.from_numpy(np.stack(rows).astype(np.float32)).to(DEV)
+    _check_codes(ms.maxsim_quantize_mx4(x), ref.quantize(x.double().cpu().numpy()))
+    # a negative zero keeps its sign
+    z = torch.full((1, 32), -0.0, device=DEV)
+    codes, scale = ms.maxsim_quantize_mx4(z)
+    assert (codes == 0x88).all() and (scale == 127).all()
+
+
+def test_quantize_normalized_ties(ms):
+    """Rows whose norm is a whole number put values exactly on borders and powers of two."""
+    rows = np.zeros((8, 64))
+    rows[0, 5] = 3.0                                   # 1
+    rows[1, [1, 2, 40, 41]] = [2, -2, 2, 2]            # 1/2 each
+    rows[2, 0] = 5; rows[2, 1:40] = 1                  # norm 8: 5/8 and 1/8 in one block
+    rows[3, 0] = 7; rows[3, 1:16] = 1                  # norm 8: 7/8
+    rows[4, :16] = 1                                   # 1/4
+    rows[5, 0] = 25; rows[5, 1] = -31; rows[5, 2] = 3; rows[5, 3:8] = 1  # norm 40: 25/40 = 5/8
+    rows[5, 0:10] = [25, 31, 3, 1, 1, 1, 1, 1, 0, 0]
+    rows[6, :64] = 1                                   # 1/8
+    rows[7, 0] = 3; rows[7, 33] = -4                   # 3/5, 4/5
+    for f in (1.0, 2.0 ** 90, 2.0 ** -100):
+        x = torch.from_numpy(rows * f).float().to(DEV)
+        _check_codes(ms.maxsim_quantize_mx4(x, normalize=True), ref.quantize(x.double().cpu().numpy(), normalize=True))
+    x = torch.from_numpy(rows).to(torch.bfloat16).to(DEV)
+    _check_codes(ms.maxsim_quantize_mx4(x, normalize=True), ref.quantize(x.double().cpu().numpy(), normalize=True))
+
+
+def test_quantize_extremes(ms):
+    """Zeros, subnormal rows, the largest values; with and without normalisation."""
+    rows = np.zeros((9, 96), dtype=np.float32)
+    rows[1, :] = 2.0 ** -149
+    rows[2, ::3] = 2.0 ** -140
+    rows[3, :] = 3.4028234e38
+    rows[4, 0] = 3.4028234e38; rows[4, 50] = 2.0 ** -120
+    rows[5, :] = 2.0 ** -110
+    rows[6, :] = 2.0 ** -111
+    rows[7, 0] = 1.0; rows[7, 32:64] = 2.0 ** -126; rows[7, 64:] = 1e-30
+    rows[8, :] = np.linspace(1e37, 3e38, 96)
+    x = torch.from_numpy(rows).to(DEV)
+    for normalize in (False, True):
+        _check_codes(ms.maxsim_quantize_mx4(x, normalize=normalize),
+                     ref.quantize(x.double().cpu().numpy(), normalize=normalize))
+
+
+@by_type
+def test_quantize_marks_nan_and_infinity(ms, dtype):
+    x = _rows(6, 100, dtype, 3)
+    clean = x.clone()
+    x[1, 40] = float("nan")
+    x[2, 99] = float("inf")
+    x[4, 3] = -float("inf")
+    codes, scale = ms.maxsim_quantize_mx4(x)
+    c0, s0 = ms.maxsim_quantize_mx4(clean)
+    marked = torch.zeros_like(scale, dtype=torch.bool)
+    marked[1, 1] = marked[2, 3] = marked[4, 0] = True
+    assert torch.equal(scale == 255, marked)
+    assert torch.equal(scale[~marked], s0[~marked])
+    keep = (~marked).repeat_interleave(16, 1)
+    assert torch.equal(codes[keep], c0[keep])
+    codes, scale = ms.maxsim_quantize_mx4(x, normalize=True)
+    rows = torch.tensor([False, True, True, False, True, False], device=DEV)
+    assert (scale[rows] == 255).all()
+    c0, s0 = ms.maxsim_quantize_mx4(clean, normalize=True)
+    assert torch.equal(scale[~rows], s0[~rows]) and torch.equal(codes[~rows], c0[~rows])
+    mask = (~rows).to(torch.uint8)
+    for normalize in (False, True):  # masked rows are not looked at
+        codes, scale = ms.maxsim_quantize_mx4(x, mask, normalize=normalize)
+        assert (scale[rows] == 127).all() and (codes[rows] == 0).all() and not (scale == 255).any()
+
+
+@by_type
+def test_dequantize_every_code_and_scale(ms, dtype):
+    codes = torch.arange(16, device=DEV).repeat(2).view(1, 32)
+    codes = (codes[:, 0::2] | codes[:, 1::2] << 4).to(torch.uint8).repeat(256, 1).contiguous()
+    scale = torch.arange(256, device=DEV).to(torch.uint8).view(256, 1)
+    want = torch.from_numpy(ref.values(codes.cpu().numpy(), scale.cpu().numpy())).to(dtype)
+    got = ms.maxsim_dequantize_mx4(codes, scale, out_dtype=dtype).cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    assert torch.equal(got[fine], want[fine])
+
+
+@by_type
+@pytest.mark.parametrize("T,d", ROWS)
+def test_dequantize(ms, T, d, dtype):
+    codes, scale = _random_mx4((T,), d, d)
+    Y, ok = _guarded((T, d), dtype, -7.0)
+    ms.maxsim_dequantize_mx4(codes, scale, d, Y=Y)
+    torch.cuda.synchronize()
+    assert ok()
+    assert torch.equal(Y.double(), _values(codes, scale)[:, :d].to(dtype).double())
+
+
+def test_rows_beyond_32_bit_offsets(ms):
+    T, d = (1 << 32) // 256 + 9, 256
+    x = torch.zeros(T, d, dtype=torch.float16, device=DEV)
+    x[-9:] = _rows(9, d, torch.float16, 4)
+    for normalize in (False, True):
+        codes, scale = ms.maxsim_quantize_mx4(x, normalize=normalize)
+        _check_codes((codes[-9:], scale[-9:]), ref.quantize(x[-9:].double().cpu().numpy(), normalize=normalize))
+    y = ms.maxsim_dequantize_mx4(codes, scale, out_dtype=torch.float16)
+    assert torch.equal(y[-9:].double(), _values(codes[-9:], scale[-9:]).half().double())
+
+
+# ------------------------------------------------------------- product
+
+LINEAR = [(1, 1, 1), (1, 16, 32), (2, 100, 33), (16, 3, 100), (17, 64, 768), (32, 257, 1000), (33, 128, 768), (1, 512, 4096),
+          (40, 1, 64), (64, 64, 256), (65, 63, 257), (100, 200, 300), (130, 96, 1056), (300, 1001, 1000), (513, 128, 4096),
+          (70, 70, 8192), (5, 33, 9000), (200, 40, 33)]
+
+
+def _linear_want(A, As, W, Ws, bias):
+    a, w = _values(A, As), _values(W, Ws)
+    y = a @ w.T.contiguous()
+    mag = a.abs() @ w.abs().T.contiguous()
+    return (y if bias is None else y + bias.double()).cpu().numpy(), mag.cpu().numpy()
+
+
+def _within(name, got, want, bound):
+    off = np.abs(got.double().cpu().numpy() - want)
+    bad = ~(off <= bound)
+    assert not bad.any(), f"{name}: {bad.sum()} beyond the bound, first at {np.argwhere(bad)[0]}: " \
+                          f"off {off[bad][0]:.3e}, bound {np.broadcast_to(bound, off.shape)[bad][0]:.3e}"
+
+
+@pytest.mark.parametrize("T,N,K", LINEAR)
+def test_linear(ms, T, N, K):
+    A, As = _random_mx4((T,), K, T + K, spread=6)
+    W, Ws = _random_mx4((N,), K, N + K + 1, spread=6)
+    for dtype, with_bias in ((torch.bfloat16, False), (torch.float16, True), (torch.float32, True)):
+        bias = torch.randn(N, generator=_gen(N), device=DEV) if with_bias else None
+        want, mag = _linear_want(A, As, W, Ws, bias)
+        Y, ok = _guarded((T, N), dtype, -7.0)
+        ms.maxsim_linear_mx4(A, As, W, Ws, bias, Y=Y)
+        torch.cuda.synchronize()
+        assert ok()
+        b = 0.0 if bias is None else bias.double().cpu().numpy()
+        fits = np.abs(want) < 60000 if dtype == torch.float16 else np.ones_like(want, bool)
+        _within(str(dtype), torch.where(torch.from_numpy(fits).to(DEV), Y, 0), np.where(fits, want, 0),
+                ref.linear_bound(want, mag, K, b, dtype))
+    if As.numel() > 1:  # exponents at odd addresses
+        assert torch.equal(ms.maxsim_linear_mx4(A, _off_by_one(As), W, _off_by_one(Ws), bias, out_dtype=torch.float32), Y)
+
+
+@pytest.mark.parametrize("T,N,K", [(4096, 4096, 320), (2048, 4100, 512), (4100, 4099, 200)])
+def test_linear_large_tiles(ms, T, N, K):
+    A, As = _random_mx4((T,), K, 5, spread=3)
+    W, Ws = _random_mx4((N,), K, 6, spread=3)
+    want, mag = _linear_want(A, As, W, Ws, None)
+    got = ms.maxsim_linear_mx4(A, As, W, Ws, out_dtype=torch.float32)
+    _within("fp32", got, want, ref.linear_bound(want, mag, K, 0.0, torch.float32))
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_linear_nan_blocks_and_far_exponents(ms, T):
+    K, N = 200, 70
+    A, As = _random_mx4((T,), K, 1)
+    W, Ws = _random_mx4((N,), K, 2)
+    As[1, 3] = 255
+    A[1, 48:64] = 0  # a block of zeros is NaN all the same
+    Ws[5, 0] = 255
+    Ws[6] = 0
+    Ws[7] = 240
+    y = ms.maxsim_linear_mx4(A, As, W, Ws, out_dtype=torch.float32)
+    nan = torch.isnan(y)
+    want = torch.zeros_like(nan)
+    want[1] = True
+    want[:, 5] = True
+    assert torch.equal(nan, want)
+    ref_y, mag = _linear_want(A, As, W, Ws, None)
+    ok = ~want.cpu().numpy()
+    bound = ref.linear_bound(ref_y, mag, K, 0.0, torch.float32)
+    # products far below the others' range are subnormal sums: each addition rounds to 2^-149
+    off = np.abs(y.double().cpu().numpy() - ref_y)
+    assert (off[ok] <= bound[ok] + 64 * 2.0 ** -149).all()
+
+
+def test_linear_rows_beyond_32_bit_offsets(ms):
+    T, K, N = (1 << 33) // 16384 + 40, 16384 * 2, 40
+    A = torch.zeros(T, K // 2, dtype=torch.uint8, device=DEV)
+    As = torch.full((T, K // 32), 127, dtype=torch.uint8, device=DEV)
+    A[-70:], As[-70:] = _random_mx4((70,), K, 1)
+    W, Ws = _random_mx4((N,), K, 2)
+    y = ms.maxsim_linear_mx4(A, As, W, Ws, out_dtype=torch.float32)
+    want, mag = _linear_want(A[-70:], As[-70:], W, Ws, None)
+    _within("last rows", y[-70:], want, ref.linear_bound(want, mag, K, 0.0, torch.float32))
+    assert (y[:-70] == 0).all()
+
+
+# ------------------------------------------------------------- scores
+
+SCORE = [(1, 32, 3, 180, 128), (1, 1, 1, 1, 1), (2, 5, 7, 33, 31), (3, 20, 50, 77, 80), (1, 32, 300, 50, 128),
+         (5, 33, 9, 64, 128), (9, 32, 40, 100, 128), (40, 7, 3, 31, 64), (2, 300, 5, 90, 128), (1, 1024, 4, 257, 128),
+         (3, 70, 6, 45, 256), (2, 40, 10, 64, 384), (2, 32, 20, 70, 768), (2, 33, 5, 40, 1024), (1, 16, 4, 100, 1000),
+         (3, 65, 4, 50, 200), (2, 260, 3, 40, 512), (1, 32, 2, 20000, 128), (2, 8, 70, 600, 96), (17, 16, 2, 2500, 128)]
+
+
+def _check_scores(ms, Q, Qs, D, Ds, qm, dm, d, exact):
+    Nq, Lq = Qs.shape[:2]
+    Nd, Ld = Ds.shape[:2]
+    want, sim, mag = ref.maxsim(_values(Q, Qs), _values(D, Ds), qm, dm)
+    scores, ok1 = _guarded((Nq, Nd), torch.float32, -7.0)
+    argmax, ok2 = _guarded((Nq, Nd, Lq), torch.int32, -7)
+    ms.maxsim_fwd_mx4(Q, Qs, D, Ds, qm, dm, scores=scores, argmax=argmax)
+    plain, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, qm, dm)
+    torch.cuda.synchronize()
+    assert ok1() and ok2()
+    best = sim.amax(3)
+    live = best > -np.inf
+    err = torch.where(live, torch.from_numpy(ref.sim_error(mag.amax(3).cpu().numpy(), d)).to(DEV), 0.0)
+    size = torch.where(live, best.abs(), 0.0)
+    bound = err.sum(2) + 1.01 * (Lq + 8) * ref.U * size.sum(2) + ref.U * want.abs()
+    for got in (scores, plain):
+        if exact:
+            assert torch.equal(got.double(), want)
+        else:
+            assert ((got.double() - want).abs() <= bound).all()
+    a = argmax.long()
+    assert ((a >= 0) & (a < Ld)).all()
+    assert (a[~live] == 0).all()
+    picked = sim.gather(3, a[..., None])[..., 0]
+    first = (sim == best[..., None]).int().argmax(3)
+    if exact:
+        assert torch.equal(a[live], first[live])
+    else:
+        assert (picked >= best - 2 * err)[live].all()
+
+
+@pytest.mark.parametrize("Nq,Lq,Nd,Ld,d", SCORE)
+def test_scores(ms, Nq, Lq, Nd, Ld, d):
+    for spread in (1, 5):  # one exponent: sums are exact, ties are many
+        Q, Qs = _random_mx4((Nq, Lq), d, Lq + d, spread)
+        D, Ds = _random_mx4((Nd, Ld), d, Ld + d, spread)
+        _check_scores(ms, Q, Qs, D, Ds, None, None, d, spread == 1)
+        qm, dm = _mask((Nq, Lq), 1), _mask((Nd, Ld), 2)
+        dm[Nd // 2] = 0                                  # a document without a token
+        if Nd > 2:
+            dm[0, Ld // 2:] = 0                          # a padded one
+            dm[1, :] = 0
+            dm[1, Ld - 1] = 1                            # only the last token
+        _check_scores(ms, Q, Qs, D, Ds, qm, dm, d, spread == 1)
+    s, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, qm, dm)
+    t, _ = ms.maxsim_fwd_mx4(Q, _off_by_one(Qs), D, _off_by_one(Ds), _off_by_one(qm), _off_by_one(dm))
+    assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("Nq,Lq,Nd,Ld", [(1, 32, 6, 70), (9, 40, 6, 70)])
+def test_scores_nan(ms, Nq, Lq, Nd, Ld):
+    """A NaN block shows in the scores that its token enters, and only there."""
+    d = 128
+    Q, Qs = _random_mx4((Nq, Lq), d, 1)
+    D, Ds = _random_mx4((Nd, Ld), d, 2)
+    clean, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds)
+    Ds[2, 5, 1] = 255
+    D[2, 5] = 0
+    for want_argmax in (False, True):
+        s, a = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, want_argmax=want_argmax)
+        assert torch.isnan(s[:, 2]).all()
+        keep = torch.arange(Nd, device=DEV) != 2
+        assert torch.equal(s[:, keep], clean[:, keep])
+        if a is not None:
+            assert ((a >= 0) & (a < Ld)).all()
+    dm = torch.ones(Nd, Ld, dtype=torch.uint8, device=DEV)
+    dm[2, 5] = 0
+    s, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm)
+    assert not torch.isnan(s).any()
+    Qs[0, 3, 0] = 255
+    s, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm)
+    assert torch.isnan(s[0]).all() and not torch.isnan(s[1:]).any()
+    qm = torch.ones(Nq, Lq, dtype=torch.uint8, device=DEV)
+    qm[0, 3] = 0
+    s, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, qm, dm)
+    assert not torch.isnan(s).any()
+
+
+def test_scores_without_tokens(ms):
+    for Nq, Lq, Nd, Ld in ((2, 0, 3, 5), (2, 4, 3, 0), (0, 4, 3, 5), (2, 4, 0, 5), (2, 0, 3, 0)):
+        Q, Qs = _random_mx4((Nq, Lq), 64, 1)
+        D, Ds = _random_mx4((Nd, Ld), 64, 2)
+        s, a = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, want_argmax=True)
+        assert s.shape == (Nq, Nd) and (s == 0).all() and (a == 0).all()
+
+
+def test_scores_beyond_32_bit_offsets(ms):
+    Nd, Ld, d = 70000, 1000, 128
+    D = torch.zeros(Nd, Ld, d // 2, dtype=torch.uint8, device=DEV)
+    Ds = torch.full((Nd, Ld, d // 32), 127, dtype=torch.uint8, device=DEV)
+    D[-3:], Ds[-3:] = _random_mx4((3, Ld), d, 1)
+    Q, Qs = _random_mx4((2, 32), d, 2)
+    s, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds)
+    want, _, _ = ref.maxsim(_values(Q, Qs), _values(D[-3:], Ds[-3:]))
+    assert torch.allclose(s[:, -3:].double(), want, rtol=1e-5, atol=0)
+    assert (s[:, :-3] == 0).all()
+
+
+# ------------------------------------------------------------- refusals, streams, graphs, runs
+
+def test_refusals(ms):
+    Q, Qs = _random_mx4((2, 4), 64, 1)
+    x = torch.zeros(4, 64, device=DEV)
+    for call in (lambda: ms.maxsim_quantize_mx4(x.t()),
+                 lambda: ms.maxsim_quantize_mx4(x.cpu()),
+                 lambda: ms.maxsim_quantize_mx4(x.int()),
+                 lambda: ms.maxsim_quantize_mx4(x, torch.ones(3, dtype=torch.uint8, device=DEV)),
+                 lambda: ms.maxsim_dequantize_mx4(Q, Qs, 100),
+                 lambda: ms.maxsim_dequantize_mx4(Q, Qs[:, :, :1], 64),
+                 lambda: ms.maxsim_dequantize_mx4(Q, Qs, out_dtype=torch.int8),
+                 lambda: ms.maxsim_linear_mx4(Q, Qs, Q, Qs),
+                 lambda: ms.maxsim_linear_mx4(Q, Qs, Q[0, :, :16].contiguous(), Qs[0, :, :1].contiguous()),
+                 lambda: ms.maxsim_linear_mx4(Q, Qs, Q[0], Qs[0], torch.zeros(5, device=DEV)),
+                 lambda: ms.maxsim_fwd_mx4(Q, Qs, Q[0], Qs[0]),
+                 lambda: ms.maxsim_fwd_mx4(Q, Qs, Q, Qs, torch.ones(2, 5, dtype=torch.uint8, device=DEV)),
+                 lambda: ms.maxsim_fwd_mx4(Q, Qs, Q.cpu(), Qs.cpu()),
+                 lambda: ms.maxsim_fwd_mx4(Q.char(), Qs, Q, Qs)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(ms.MaxSimError):  # 2048 channels
+        B, Bs = _random_mx4((1, 2), 2048, 1)
+        ms.maxsim_fwd_mx4(B, Bs, B, Bs)
+    with pytest.raises(ms.MaxSimError):  # codes at an address that 16 does not divide
+        ms.maxsim_dequantize_mx4(_off_by_one(Q), Qs)
+
+
+def test_side_streams(ms):
+    """Calls on streams of their own, outputs allocated there."""
+    Q, Qs = _random_mx4((3, 32), 128, 1)
+    Ds = [_random_mx4((200, 90), 128, 5 + i) for i in range(2)]
+    want = [ms.maxsim_fwd_mx4(Q, Qs, *D)[0] for D in Ds]
+    streams = [torch.cuda.Stream() for _ in Ds]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = [ms.maxsim_fwd_mx4(Q, Qs, *D, stream=s)[0] for D, s in zip(Ds, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_serving_run(ms):
+    """Hidden states to 4-bit embeddings, scan, top-k and exact rescoring: each
+    step against float64 of the step's own inputs; then captured and replayed."""
+    d, K, Nd, Ld, Nq, Lq = 128, 384, 60, 50, 4, 32
+    Wf = torch.randn(d, K, generator=_gen(1), device=DEV) / K ** 0.5
+    W, Ws = ms.maxsim_quantize_mx4(Wf)
+    hd, hq = _rows(Nd * Ld, K, torch.bfloat16, 2).view(Nd, Ld, K), _rows(Nq * Lq, K, torch.bfloat16, 3).view(Nq, Lq, K)
+    dm = _mask((Nd, Ld), 4)
+
+    def run():
+        D, Dsc = ms.embed_tokens_mx4(hd, W, Ws, mask=dm)
+        Q, Qsc = ms.embed_tokens_mx4(hq, W, Ws)
+        Df = ms.maxsim_dequantize_mx4(D, Dsc, d)
+        Qf = ms.maxsim_dequantize_mx4(Q, Qsc, d)
+        doc, val, scan = ms.two_stage_topk_mx4(Q, Qsc, D, Dsc, Qf, Df, 5, 20, None, dm)
+        return D, Dsc, Q, Qsc, doc, val, scan
+
+    D, Dsc, Q, Qsc, doc, val, scan = run()
+    a, asc = ms.maxsim_quantize_mx4(hd, dm)
+    y = ms.maxsim_linear_mx4(a, asc, W, Ws, out_dtype=torch.float32)
+    _check_codes((D.view(-1, d // 2), Dsc.view(-1, d // 32)),
+                 ref.quantize(y.view(-1, d).double().cpu().numpy(), dm.view(-1).cpu().numpy(), True))
+    want, _, _ = ref.maxsim(_values(Q, Qsc), _values(D, Dsc), None, dm)
+    assert torch.allclose(scan.double(), want, rtol=1e-5, atol=1e-5)
+    # the embeddings are exact in 16 bits, so that rescoring gives the scan's scores again
+    top = want.topk(5, 1)
+    assert torch.allclose(val.double(), top.values, rtol=1e-5, atol=1e-5)
+    assert torch.allclose(want.gather(1, doc.long()), top.values, rtol=1e-5, atol=1e-5)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in range(4):
+        hd.mul_(-1.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, z in zip(out, run()):
+            assert torch.equal(x, z)
+
+
+def test_bitwise_repeatable(ms):
+    Q, Qs = _random_mx4((5, 70), 128, 1, 6)
+    D, Ds = _random_mx4((300, 100), 128, 2, 6)
+    A, As = _random_mx4((700,), 1000, 3, 6)
+    first = None
+    for _ in range(5):
+        out = (*ms.maxsim_fwd_mx4(Q, Qs, D, Ds, want_argmax=True), ms.maxsim_linear_mx4(A, As, A[:90], As[:90]),
+               ms.maxsim_linear_mx4(A[:9], As[:9], A[:90], As[:90]))
+        first = first or out
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
