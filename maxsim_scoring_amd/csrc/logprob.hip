@@ -8,16 +8,15 @@
 // chunk (one wave up to 1024 columns) finish there; otherwise a second launch joins
 // the chunks of a row. Few long rows spread over the card in this way.
 //
-// Best columns. Scores map to 32-bit keys in float order, and with the column behind
-// them to numbers that are all different, whose order is that of the output. A
-// histogram of 256 equal bins between the chunk's least and largest key finds the
-// bin of the k-th; it is cut into 256 again only while more than k + k/2 + 32 lie
-// at or above its lower edge. What is left is ordered by counting, for each, how
-// many are larger.
+// The sums take 2^t with t = (x - m) scale log2(e) from the hardware, off by 4 units
+// of 2^-24 |z| for the three roundings of t; they are float64, so that a row whose
+// largest probability is close to 1 keeps its entropy.
 //
-// exp is the hardware's 2^x with the rounding of x log2(e) put back (off by about
-// 2^-23 relative); sums are float64, so that a row whose largest probability is
-// close to 1 keeps its entropy.
+// Best columns. Scores map to 32-bit keys in float order. A histogram of 256 equal
+// bins between the chunk's least and largest key finds the bin of the k-th; it is
+// cut into 256 again only while more than k + k/2 + 32 lie at or above its lower
+// edge. Equal keys that are too many are told apart by their columns in the same
+// way. What is left is ordered by counting, for each, how many are larger.
 //
 // Backward. One pass, element-wise but for the targets: their gradients are added
 // into a chunk of columns in LDS by one wave, in the order of the targets.
@@ -30,27 +29,23 @@ namespace {
 
 constexpr int kBins = 256;
 constexpr int kMaxCap = 2048;     // logprob_cap(1024) and more, a power of two
-constexpr uint32_t kNanKey = 0xffffffffu;
+constexpr int kJoinThreads = 512;
+constexpr int kJoinHeld = 16;     // candidates that a thread of the join holds
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
 template <int E> constexpr int elem_bytes() { return E == kF32 ? 4 : 2; }
 
-// Keys in float order; 0 for what is no candidate (its key would be that of -Inf
-// or below), the largest for NaN. -0 ranks with +0.
+// Keys in float order, -0 as +0. (A NaN may have any key: a row that holds one is
+// marked by its largest score.)
 __device__ __forceinline__ uint32_t key_of(float v)
 {
-    uint32_t b = __builtin_bit_cast(uint32_t, v);
-    if (v != v) return kNanKey;
-    if (v == -__builtin_inff()) return 0;
-    if (v == 0.0f) b = 0;
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-// The score of a key, -Inf of 0.
 __device__ __forceinline__ float score_of(uint32_t k)
 {
-    if (k == 0) return -__builtin_inff();
     return __builtin_bit_cast(float, (k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
@@ -67,26 +62,26 @@ __device__ __forceinline__ float exp_neg(float z)
 }
 __device__ __forceinline__ float floor_z(float z) { return z < -200.0f ? -200.0f : z; }
 
-// A row's columns c0 + place, 16 per thread of T: value v of a thread is column
+// A row's columns c0 + place, N per thread of T: value v of a thread is column
 // place(v) of the chunk; V consecutive ones come in one load.
-template <int E, int T>
+template <int E, int T, int N>
 struct Layout {
     static constexpr int V = E == kF32 ? 4 : 8;
-    static constexpr int kColumns = T * kLpValues;
+    static constexpr int kColumns = T * N;
     __device__ static __forceinline__ int place(int v) { return ((v / V) * T + (int)threadIdx.x) * V + v % V; }
 };
 
 // The thread's columns of row i from c0 on: NaN-free loading of what exists and is
 // not masked, -Inf elsewhere.
-template <int E, int T>
-__device__ __forceinline__ void load_columns(const LogprobArgs& a, int64_t i, int c0, float (&x)[kLpValues])
+template <int E, int T, int N>
+__device__ __forceinline__ void load_columns(const LogprobArgs& a, int64_t i, int c0, float (&x)[N])
 {
-    typedef Layout<E, T> Y;
+    typedef Layout<E, T, N> Y;
     const int n = a.Nd - c0 < Y::kColumns ? a.Nd - c0 : Y::kColumns;
     const char* p = (const char*)a.X + (i * a.Nd + c0) * elem_bytes<E>();
     const uint8_t* mp = a.mask ? a.mask + i * a.Nd + c0 : nullptr;
 #pragma unroll
-    for (int g = 0; g < kLpValues / Y::V; ++g) {
+    for (int g = 0; g < N / Y::V; ++g) {
         const int at = Y::place(g * Y::V);
         u32x4 w = {0, 0, 0, 0};
         uint32_t keep[Y::V / 4];
@@ -129,25 +124,75 @@ __device__ __forceinline__ float load_one(const LogprobArgs& a, int64_t i, int c
     }
 }
 
-// Reductions over a workgroup of T threads, the same result in every thread. `red`
-// is LDS of T / 64 values; a barrier lies before its next use.
-template <int T, typename V, typename OP>
-__device__ __forceinline__ V block_reduce(V v, V* red, OP op)
+// Reductions over a wave, the same result in every lane: rows of 16 lanes by DPP,
+// the four rows through scalar registers.
+template <int CTRL, typename V>
+__device__ __forceinline__ V dpp_of(V v)
 {
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) v = op(v, __shfl_xor(v, m, 64));
-    if constexpr (T > 64) {
-        __syncthreads();
-        if (lane_id() == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
+    if constexpr (sizeof(V) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, false);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, false);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    } else {
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+    }
+}
+template <typename V>
+__device__ __forceinline__ V lane_of(V v, int lane)
+{
+    if constexpr (sizeof(V) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    } else {
+        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+    }
+}
+template <typename V, typename OP>
+__device__ __forceinline__ V wave_reduce(V v, OP op)
+{
+    v = op(v, dpp_of<0xB1>(v));   // quad_perm [1,0,3,2]
+    v = op(v, dpp_of<0x4E>(v));   // quad_perm [2,3,0,1]
+    v = op(v, dpp_of<0x141>(v));  // row_half_mirror
+    v = op(v, dpp_of<0x140>(v));  // row_mirror
+    return op(op(lane_of(v, 0), lane_of(v, 16)), op(lane_of(v, 32), lane_of(v, 48)));
+}
+struct AddOp { template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a + b; } };
+struct MinOp { __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; } };
+// the maximum that is NaN where either is
+struct MaxOp { __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); } };
+
+// Sums of lanes 0 .. l: within rows of 16 lanes by row_shr, then the last lane of
+// each row (of each half) to the next.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v)
+{
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, true);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+    return v;
+}
+
+// The waves' results joined in order; put by one lane of each wave, a barrier between.
+template <int W, typename V>
+__device__ __forceinline__ void put(V (&red)[W], V v)
+{
+    if (W > 1 && lane_id() == 0) red[threadIdx.x >> 6] = v;
+}
+template <int W, typename V, typename OP>
+__device__ __forceinline__ V joined(const V (&red)[W], V v, OP op)
+{
+    if constexpr (W > 1) {
         v = red[0];
 #pragma unroll
-        for (int w = 1; w < T / 64; ++w) v = op(v, red[w]);
+        for (int w = 1; w < W; ++w) v = op(v, red[w]);
     }
     return v;
 }
-struct AddOp { template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a + b; } };
-struct MaxOp { template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a > b ? a : b; } };
 
 // Order of the output as a number: the key, then the lower column first. All of a
 // row's are different.
@@ -161,22 +206,23 @@ __device__ __forceinline__ int column_of(uint64_t o, int cbits)
     return (int)(m - ((uint32_t)o & m));
 }
 
-// A bound such that at least K and at most cap of a set of numbers, all different
-// and between lo and hi, are at or above it (the set has more than cap, cap >= K).
-// each(f) calls f(number) for each of this thread's. hist: LDS of kBins + 2.
-template <int T, typename Each>
-__device__ __forceinline__ uint64_t select_bound(Each each, uint32_t K, uint32_t cap, uint64_t lo, uint64_t hi, uint32_t* hist)
+// A bound of a set of numbers between lo and hi such that at least K of them, with
+// `above` others beyond hi, are at or above it; upto becomes how many. That is at
+// most cap, or the bound is the K-th largest itself. each(f) calls f(number) for
+// each of this thread's. hist: LDS of kBins + 3.
+template <int T, typename U, typename Each>
+__device__ __forceinline__ U select_bound(Each each, uint32_t K, uint32_t cap, U lo, U hi, uint32_t& above, uint32_t& upto,
+                                          uint32_t* hist)
 {
-    int width = 64 - __builtin_clzll((hi - lo) | 1);  // [lo, lo + 2^width) holds them
-    uint32_t above = 0;                               // numbers beyond that range
+    int shift = 64 - __builtin_clzll((uint64_t)(hi - lo) | 1) - 8;  // 256 bins of 2^shift cover them
+    if (shift < 0) shift = 0;
+    U bins = kBins;
     for (;;) {
-        const int shift = width > 8 ? width - 8 : 0;
-        const uint64_t end = width < 64 ? lo + ((uint64_t)1 << width) : 0;  // 0: none
-        __syncthreads();
         for (int k = threadIdx.x; k < kBins; k += T) hist[k] = 0;
         __syncthreads();
-        each([&](uint64_t o) {
-            if (o >= lo && (end == 0 || o < end)) atomicAdd(&hist[(o - lo) >> shift], 1u);
+        each([&](U o) {
+            const U bin = (U)(o - lo) >> shift;
+            if (o >= lo && bin < bins) atomicAdd(&hist[(uint32_t)bin], 1u);
         });
         __syncthreads();
         if (threadIdx.x < 64) {
@@ -185,47 +231,139 @@ __device__ __forceinline__ uint64_t select_bound(Each each, uint32_t K, uint32_t
             uint32_t c[4], mine = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) mine += c[e] = hist[255 - (4 * lane + e)];
-            uint32_t incl = mine;
-#pragma unroll
-            for (int off = 1; off < 64; off *= 2) {
-                const uint32_t v = __shfl_up(incl, off, 64);
-                if (lane >= off) incl += v;
-            }
-            uint32_t before = above + incl - mine;
-            uint32_t bin = 0, over = 0, upto = 0;
+            uint32_t before = above + wave_scan(mine) - mine;
+            uint32_t bin = 0, over = 0, up = 0;
             bool found = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (before < K && K <= before + c[e]) {
                     bin = (uint32_t)(255 - (4 * lane + e));
                     over = before;
-                    upto = before + c[e];
+                    up = before + c[e];
                     found = true;
                 }
                 before += c[e];
             }
-            if (found) {  // one lane; all lanes have read their bins
+            if (found) {  // one lane
                 hist[kBins] = bin;
                 hist[kBins + 1] = over;
-                hist[kBins + 2] = upto;
+                hist[kBins + 2] = up;
             }
         }
         __syncthreads();
-        lo += (uint64_t)hist[kBins] << shift;
+        lo += (U)hist[kBins] << shift;
         above = hist[kBins + 1];
-        if (hist[kBins + 2] <= cap || shift == 0) return lo;
-        width = shift;
+        upto = hist[kBins + 2];
+        if (upto <= cap || shift == 0) return lo;
+        bins = shift < 8 ? (U)1 << shift : (U)kBins;  // the bin and nothing beyond it
+        shift = shift > 8 ? shift - 8 : 0;
     }
 }
 
-// Writes the K best of n <= kMaxCap numbers of cand (LDS) in order; z and L give
-// their log probabilities.
+// What the best columns are picked from, value by value (for_all calls f(v) as often
+// in every lane): N scores of a thread's columns, N numbers in registers, or numbers in
+// memory. above: is value v a candidate whose key is at least the bound's?
+struct Bound {
+    uint32_t key;
+    float x;          // its score
+    uint64_t number;  // the least with that key
+};
+template <int E, int T, int N>
+struct Scores {
+    const float (&x)[N];
+    int c0, cbits;
+    template <typename F> __device__ __forceinline__ void for_all(F f) const { static_for<0, N>(f); }
+    __device__ __forceinline__ bool is(int v) const { return x[v] > -__builtin_inff(); }
+    __device__ __forceinline__ uint32_t key(int v) const { return key_of(x[v]); }
+    __device__ __forceinline__ uint64_t number(int v) const { return order_of(key(v), c0 + Layout<E, T, N>::place(v), cbits); }
+    __device__ __forceinline__ bool above(int v, const Bound& b) const { return x[v] >= b.x; }
+};
+template <int N>
+struct Numbers {
+    const uint64_t (&o)[N];
+    int cbits;
+    template <typename F> __device__ __forceinline__ void for_all(F f) const { static_for<0, N>(f); }
+    __device__ __forceinline__ bool is(int v) const { return o[v] != 0; }
+    __device__ __forceinline__ uint32_t key(int v) const { return (uint32_t)(o[v] >> cbits); }
+    __device__ __forceinline__ uint64_t number(int v) const { return o[v]; }
+    __device__ __forceinline__ bool above(int v, const Bound& b) const { return o[v] >= b.number; }
+};
+struct Far {
+    const uint64_t* o;
+    int n, stride, cbits;
+    template <typename F> __device__ __forceinline__ void for_all(F f) const
+    {
+        for (int v = 0; v * stride < n; ++v) f(v);
+    }
+    __device__ __forceinline__ uint64_t number(int v) const
+    {
+        const int e = v * stride + (int)threadIdx.x;
+        return e < n ? o[e] : 0;
+    }
+    __device__ __forceinline__ bool is(int v) const { return number(v) != 0; }
+    __device__ __forceinline__ uint32_t key(int v) const { return (uint32_t)(number(v) >> cbits); }
+    __device__ __forceinline__ bool above(int v, const Bound& b) const { return number(v) >= b.number; }
+};
+
+// Picks the best columns into to[0, n), n <= cap, in any order. least, top: the range
+// of the candidates' keys; have: how many there are in all. counter: 0.
+template <int T, typename Source>
+__device__ __forceinline__ uint32_t pick(const Source& from, int have, uint32_t least, uint32_t top, const LogprobArgs& a,
+                                         uint64_t* to, uint32_t* hist, uint32_t* counter)
+{
+    const uint32_t K = (uint32_t)a.K, cap = (uint32_t)a.cap;
+    uint32_t key = least, above = 0, upto = (uint32_t)have;
+    uint64_t border = 0;  // of the numbers that are taken, where equal keys are told apart
+    if (upto > cap) {
+        key = select_bound<T, uint32_t>(
+            [&](auto f) {
+                from.for_all([&](int v) {
+                    if (from.is(v)) f(from.key(v));
+                });
+            },
+            K, cap, least, top, above, upto, hist);
+        if (upto > cap)
+            border = select_bound<T, uint64_t>(
+                [&](auto f) {
+                    from.for_all([&](int v) {
+                        if (from.is(v) && from.key(v) == key) f(from.number(v));
+                    });
+                },
+                K, cap, order_of(key, a.Nd - 1, a.cbits), order_of(key, 0, a.cbits), above, upto, hist);
+    }
+    const Bound b = {key, score_of(key), (uint64_t)key << a.cbits};
+    // a wave takes a run of places; which one depends on the waves' timing, the
+    // outputs do not: they are ordered later
+    auto copy = [&](auto taken) {
+        uint32_t mine = 0;
+        from.for_all([&](int v) { mine += (uint32_t)__builtin_popcountll(__ballot(taken(v))); });
+        if (mine == 0) return;
+        uint32_t at = 0;
+        if (lane_id() == 0) at = atomicAdd(counter, mine);
+        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        from.for_all([&](int v) {
+            const bool t = taken(v);
+            const uint64_t all = __ballot(t);
+            if (all == 0) return;
+            const uint32_t place = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+            if (t && place < cap) to[place] = from.number(v);
+            at += (uint32_t)__builtin_popcountll(all);
+        });
+    };
+    if (border == 0) copy([&](int v) { return from.above(v, b); });
+    else copy([&](int v) { return from.is(v) && from.number(v) >= border; });
+    __syncthreads();
+    return *counter < cap ? *counter : cap;
+}
+
+// Writes the K best of n <= kMaxCap numbers of cand (LDS) in order.
 template <int T>
 __device__ __forceinline__ void write_best(const LogprobArgs& a, int64_t i, const uint64_t* cand, int n, float m, double L)
 {
     for (int e = threadIdx.x; e < n; e += T) {
         const uint64_t mine = cand[e];
         int place = 0;
+#pragma unroll 8
         for (int k = 0; k < n; ++k) place += cand[k] > mine;
         if (place < a.K) {
             const float x = score_of((uint32_t)(mine >> a.cbits));
@@ -239,223 +377,243 @@ __device__ __forceinline__ void write_best(const LogprobArgs& a, int64_t i, cons
     }
 }
 
-// A row's statistics. A NaN or +Inf among the candidates makes the sums NaN, and
-// with them every float output of the row.
-__device__ __forceinline__ void write_stats(const LogprobArgs& a, int64_t i, float m, double sum, double sum_z, double L)
+// A row's statistics. A NaN or +Inf among the candidates makes the sum NaN, and
+// with it every float output of the row.
+__device__ __forceinline__ double sum_of(float m, double sum)
+{
+    return m < __builtin_inff() ? sum : __builtin_nan("");
+}
+__device__ __forceinline__ void write_stats(const LogprobArgs& a, int64_t i, float m, double sum, double sum_t, double L)
 {
     a.norm[2 * i] = L == L ? m : __builtin_nanf("");
     a.norm[2 * i + 1] = (float)L;
-    if (a.entropy) a.entropy[i] = sum == 0.0 ? 0.0f : (float)(L - sum_z / sum);
+    if (a.entropy) a.entropy[i] = sum == 0.0 ? 0.0f : (float)(L - sum_t * 0x1.62e42fefa39efp-1 / sum);  // z = t log 2
 }
 
-// Target p of a row, `before` candidates before it.
-template <int E>
-__device__ __forceinline__ void write_target(const LogprobArgs& a, int64_t i, int p, uint32_t before, float m, double L)
+// Target p of a row: column c (-1: none named) with score x (-Inf: no candidate),
+// `before` candidates before it.
+__device__ __forceinline__ void write_target(const LogprobArgs& a, int64_t i, int p, int c, float x, uint32_t before, float m, double L)
 {
-    const int c = a.targets[i * a.P + p];
-    const bool named = c >= 0 && c < a.Nd;
-    const float x = named ? load_one<E>(a, i, c) : -__builtin_inff();
     const bool in = x != -__builtin_inff();
-    float lp = named ? x : 0.0f;
+    float lp = c >= 0 ? x : 0.0f;
     if (in || L != L) lp = (float)((double)(a.scale * (x - m)) - L);
     a.logp[i * a.P + p] = lp;
     if (a.rank) a.rank[i * a.P + p] = in ? (int)before : -1;
 }
 
-// One chunk of a row. WHOLE: the row's only one.
-template <int E, int T, bool WHOLE>
+template <int E>
+__device__ __forceinline__ int target_of(const LogprobArgs& a, int64_t i, int p, float& x)
+{
+    int c = p < a.P ? a.targets[i * a.P + p] : -1;
+    if (c >= a.Nd || c < 0) c = -1;
+    x = c >= 0 ? load_one<E>(a, i, c) : -__builtin_inff();
+    return c;
+}
+
+// 2^t of scores against the largest, t at least -200 (where 2^t is 0): so for -Inf,
+// and in rows without candidates.
+__device__ __forceinline__ float t_of(float x, float m, float c) { return __builtin_fmaxf((x - m) * c, -200.0f); }
+
+// One chunk of a row, N columns a thread. WHOLE: the row's only one.
+template <int E, int T, int N, bool WHOLE>
 __global__ __launch_bounds__(T) void logprob_part_kernel(LogprobArgs a)
 {
-    typedef Layout<E, T> Y;
+    typedef Layout<E, T, N> Y;
+    constexpr int W = T / 64;
     __shared__ uint32_t hist[kBins + 4];
-    __shared__ uint64_t cand[WHOLE ? kMaxCap : 1];
-    __shared__ uint32_t red_key[4], counter;
-    __shared__ double red_sum[4];
-    __shared__ uint32_t counts[4][64];
+    __shared__ uint64_t cand[kMaxCap];
+    __shared__ float red_m[W];
+    __shared__ uint32_t red_least[W], red_have[W], counter;
+    __shared__ double red_sum[W], red_t[W];
+    __shared__ uint32_t counts[W][64];
 
     const int64_t unit = blockIdx.x, i = WHOLE ? unit : unit / a.chunks;
     const int c0 = WHOLE ? 0 : (int)(unit % a.chunks) * Y::kColumns;
-    float x[kLpValues];
-    load_columns<E, T>(a, i, c0, x);
+    const int wave = threadIdx.x >> 6, lane = lane_id();
+    if (threadIdx.x == 0) counter = 0;
+    float x[N];
+    load_columns<E, T, N>(a, i, c0, x);
+    float tx;  // target `lane`
+    int tc = target_of<E>(a, i, lane, tx);
 
-    uint32_t key[kLpValues], top = 0, least = kNanKey;
-    int have = 0;
+    float m = x[0];
+    uint32_t least = 0xffffffffu, have = 0;
 #pragma unroll
-    for (int v = 0; v < kLpValues; ++v) {
-        key[v] = key_of(x[v]);
-        top = key[v] > top ? key[v] : top;
-        if (key[v] != 0) {
-            least = key[v] < least ? key[v] : least;
-            ++have;
-        }
-    }
-    top = block_reduce<T>(top, red_key, MaxOp{});
-    const float m = score_of(top);
-    double sum = 0.0, sum_z = 0.0;
+    for (int v = 1; v < N; ++v) m = MaxOp{}(m, x[v]);
+    m = wave_reduce(m, MaxOp{});
+    put(red_m, m);
+    if (a.K) {
+        float low = __builtin_inff();
 #pragma unroll
-    for (int v = 0; v < kLpValues; ++v) {
-        const float z = floor_z(a.scale * (x[v] - m));
-        const float e = exp_neg(z);
-        if (key[v] != 0) {
-            sum += (double)e;
-            sum_z = __builtin_fma((double)e, (double)z, sum_z);
+        for (int v = 0; v < N; ++v) {
+            const bool in = x[v] > -__builtin_inff();
+            have += (uint32_t)__builtin_popcountll(__ballot(in));
+            low = in && x[v] < low ? x[v] : low;
         }
+        least = key_of(low);
+        least = wave_reduce(least, MinOp{});
+        put(red_least, least);
+        put(red_have, have);
     }
-    sum = block_reduce<T>(sum, red_sum, AddOp{});
-    sum_z = block_reduce<T>(sum_z, red_sum, AddOp{});
+    if (W > 1) __syncthreads();
+    m = joined(red_m, m, MaxOp{});
+
+    const float scale2 = a.scale * 0x1.715476p0f;  // log2(e)
+    double sum = 0.0, sum_t = 0.0;
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+        const float t = t_of(x[v], m, scale2), e = __builtin_amdgcn_exp2f(t);
+        sum += (double)e;
+        sum_t = __builtin_fma((double)e, (double)t, sum_t);
+    }
+    sum = wave_reduce(sum, AddOp{});
+    sum_t = wave_reduce(sum_t, AddOp{});
+    put(red_sum, sum);
+    put(red_t, sum_t);
 
     // ---- how many come before each target, 64 targets at a time --------------
-    const int wave = threadIdx.x >> 6, lane = lane_id();
-    auto count_before = [&](int p0, uint32_t& got) {  // got: that of target p0 + lane, in wave 0
+    auto count_before = [&](int p0) {  // that of target p0 + lane
         const int np = a.P - p0 < 64 ? a.P - p0 : 64;
-        // every lane looks its target up; then one target after another
-        const int c = lane < np ? a.targets[i * a.P + p0 + lane] : -1;
-        uint32_t kt = 0;
-        if (c >= 0 && c < a.Nd) kt = key_of(load_one<E>(a, i, c));
-        uint32_t n_mine = 0;
+        uint32_t mine = 0;
         for (int p = 0; p < np; ++p) {
-            const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)kt, p);
-            const int t = __builtin_amdgcn_readlane(c, p) - c0;  // relative to the chunk
-            if (k == 0) continue;
+            const float xt = lane_of(tx, p);
+            const int t = lane_of(tc, p) - c0;  // relative to the chunk
+            if (xt == -__builtin_inff()) continue;
             // equal scores come before the target if their column does: none of a
             // chunk behind it, all of one in front of it
             uint32_t n = 0;
             auto count = [&](auto before) {
 #pragma unroll
-                for (int v = 0; v < kLpValues; ++v) n += (uint32_t)__builtin_popcountll(__ballot(before(v)));
+                for (int v = 0; v < N; ++v) n += (uint32_t)__builtin_popcountll(__ballot(before(v)));
             };
-            if (t < 0) count([&](int v) { return key[v] > k; });
-            else if (t >= Y::kColumns) count([&](int v) { return key[v] >= k; });
-            else count([&](int v) { return key[v] > k || (key[v] == k && Y::place(v) < t); });
-            n_mine = lane == p ? n : n_mine;
+            if (t < 0) count([&](int v) { return x[v] > xt; });
+            else if (t >= Y::kColumns) count([&](int v) { return x[v] >= xt; });
+            else count([&](int v) { return x[v] > xt || (x[v] == xt && Y::place(v) < t); });
+            mine = lane == p ? n : mine;
         }
-        got = n_mine;
-        if constexpr (T > 64) {
-            __syncthreads();  // the last targets' counts are read
-            counts[wave][lane] = n_mine;
-            __syncthreads();
-            got = counts[0][lane] + counts[1][lane] + counts[2][lane] + counts[3][lane];
-        }
+        counts[wave][lane] = mine;
+    };
+    auto counted = [&] {
+        uint32_t n = counts[0][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) n += counts[w][lane];
+        return n;
     };
 
-    const double L = WHOLE ? log(sum) : 0.0;
-    if constexpr (WHOLE) {
-        if (threadIdx.x == 0) write_stats(a, i, m, sum, sum_z, L);
-        for (int p0 = 0; p0 < a.P; p0 += 64) {
-            uint32_t got = 0;
-            if (a.rank) count_before(p0, got);
-            if (wave == 0 && p0 + lane < a.P) write_target<E>(a, i, p0 + lane, got, m, L);
-        }
-    } else {
-        if (threadIdx.x == 0) {
-            a.ws_top[unit] = top;
-            a.ws_sums[2 * unit] = sum;
-            a.ws_sums[2 * unit + 1] = sum_z;
-        }
-        if (a.rank) {
-            for (int p0 = 0; p0 < a.P; p0 += 64) {
-                uint32_t got;
-                count_before(p0, got);
-                if (wave == 0 && p0 + lane < a.P) a.ws_rank[unit * a.P + p0 + lane] = got;
+    double L = 0.0;
+    for (int p0 = 0; p0 == 0 || p0 < a.P; p0 += 64) {
+        if (p0 > 0) tc = target_of<E>(a, i, p0 + lane, tx);
+        if (a.rank) count_before(p0);
+        __syncthreads();  // counts, and the sums in the first round
+        if (p0 == 0) {
+            sum = sum_of(m, joined(red_sum, sum, AddOp{}));
+            sum_t = joined(red_t, sum_t, AddOp{});
+            if constexpr (WHOLE) {
+                L = log(sum);
+                if (threadIdx.x == 0) write_stats(a, i, m, sum, sum_t, L);
+            } else if (threadIdx.x == 0) {
+                a.ws_top[unit] = m;
+                a.ws_sums[2 * unit] = sum;
+                a.ws_sums[2 * unit + 1] = sum_t;
             }
         }
+        if (wave == 0 && p0 + lane < a.P) {
+            if constexpr (WHOLE) write_target(a, i, p0 + lane, tc, tx, a.rank ? counted() : 0, m, L);
+            else if (a.rank) a.ws_rank[unit * a.P + p0 + lane] = counted();
+        }
+        if (p0 + 64 < a.P) __syncthreads();  // counts are read
     }
     if (a.K == 0) return;
 
     // ---- candidates for the best columns --------------------------------------
-    have = (int)block_reduce<T>((uint32_t)have, red_key, AddOp{});
-    least = ~block_reduce<T>(~least, red_key, MaxOp{});
-    auto number = [&](int v) { return order_of(key[v], c0 + Y::place(v), a.cbits); };
-    uint64_t bound = 0;
-    if (have > a.cap)
-        bound = select_bound<T>(
-            [&](auto f) {
-#pragma unroll
-                for (int v = 0; v < kLpValues; ++v)
-                    if (key[v] != 0) f(number(v));
-            },
-            (uint32_t)a.K, (uint32_t)a.cap, (uint64_t)least << a.cbits, order_of(top, 0, a.cbits), hist);
-    if (threadIdx.x == 0) counter = 0;
-    __syncthreads();
-    uint64_t* to = WHOLE ? cand : a.ws_cand + unit * a.cap;
-    // their places depend on the waves' timing, the outputs do not: they are ordered later
-#pragma unroll
-    for (int v = 0; v < kLpValues; ++v) {
-        const bool take = key[v] != 0 && number(v) >= bound;
-        if (take) {
-            const uint32_t at = atomicAdd(&counter, 1u);
-            if (at < (uint32_t)a.cap) to[at] = number(v);
-        }
+    have = joined(red_have, have, AddOp{});
+    least = joined(red_least, least, MinOp{});
+    const uint32_t n = pick<T>(Scores<E, T, N>{x, c0, a.cbits}, (int)have, least, key_of(m), a, cand, hist, &counter);
+    if constexpr (WHOLE) {
+        write_best<T>(a, i, cand, (int)n, m, L);
+    } else {
+        // every chunk leaves cap numbers, so that the join reads them without counts
+        for (int e = threadIdx.x; e < a.cap; e += T) a.ws_cand[unit * a.cap + e] = e < (int)n ? cand[e] : 0;
     }
-    __syncthreads();
-    if constexpr (WHOLE) write_best<T>(a, i, cand, (int)counter, m, L);
-    else if (threadIdx.x == 0) a.ws_count[unit] = counter;
 }
 
 // Joins the chunks of a row.
 template <int E>
-__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a)
+__global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs a)
 {
-    constexpr int T = 256;
+    constexpr int T = kJoinThreads, W = T / 64;
     __shared__ uint32_t hist[kBins + 4];
     __shared__ uint64_t cand[kMaxCap];
-    __shared__ uint32_t red_key[4], counter;
-    __shared__ double red_sum[4];
+    __shared__ float red_m[W];
+    __shared__ uint32_t red_least[W], red_have[W], counter;
+    __shared__ double red_sum[W], red_t[W];
 
+    if (threadIdx.x == 0) counter = 0;
     const int64_t i = blockIdx.x, u0 = i * a.chunks;
-    uint32_t top = 0;
-    for (int c = threadIdx.x; c < a.chunks; c += T) top = MaxOp{}(top, a.ws_top[u0 + c]);
-    top = block_reduce<T>(top, red_key, MaxOp{});
-    const float m = score_of(top);
-    double sum = 0.0, sum_z = 0.0;
-    for (int c = threadIdx.x; c < a.chunks; c += T) {
-        const double s = a.ws_sums[2 * (u0 + c)], sz = a.ws_sums[2 * (u0 + c) + 1];
-        const uint32_t k = a.ws_top[u0 + c];
-        if (k == 0) continue;
-        const float z = floor_z(a.scale * (score_of(k) - m));  // the chunk's largest against the row's
-        const double e = (double)exp_neg(z);
-        sum = __builtin_fma(e, s, sum);
-        sum_z = __builtin_fma(e, __builtin_fma((double)z, s, sz), sum_z);
+    const int total = a.K ? a.chunks * a.cap : 0;  // candidates, 0 where a chunk had fewer
+    const bool in_registers = total <= T * kJoinHeld;
+    const uint64_t* from = a.ws_cand + u0 * a.cap;
+    float tx;
+    int tc = target_of<E>(a, i, threadIdx.x, tx);
+    uint64_t o[kJoinHeld];
+    uint32_t least = 0xffffffffu, have = 0;
+    for (int e0 = 0; e0 < total; e0 += kJoinHeld * T) {
+#pragma unroll
+        for (int k = 0; k < kJoinHeld; ++k) {
+            const int e = e0 + k * T + (int)threadIdx.x;
+            o[k] = e < total ? from[e] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinHeld; ++k) {
+            have += o[k] != 0;
+            least = o[k] != 0 ? MinOp{}(least, (uint32_t)(o[k] >> a.cbits)) : least;
+        }
     }
-    sum = block_reduce<T>(sum, red_sum, AddOp{});
-    sum_z = block_reduce<T>(sum_z, red_sum, AddOp{});
+    float m = -__builtin_inff();
+    for (int c = threadIdx.x; c < a.chunks; c += T) m = MaxOp{}(m, a.ws_top[u0 + c]);
+    m = wave_reduce(m, MaxOp{});
+    put(red_m, m);
+    least = wave_reduce(least, MinOp{});
+    put(red_least, least);
+    have = wave_reduce(have, AddOp{});
+    put(red_have, have);
+    __syncthreads();
+    m = joined(red_m, m, MaxOp{});
+
+    const float scale2 = a.scale * 0x1.715476p0f;
+    double sum = 0.0, sum_t = 0.0;
+    for (int c = threadIdx.x; c < a.chunks; c += T) {
+        const float t = t_of(a.ws_top[u0 + c], m, scale2);
+        const double e = (double)__builtin_amdgcn_exp2f(t), s = a.ws_sums[2 * (u0 + c)];
+        sum = __builtin_fma(e, s, sum);
+        sum_t = __builtin_fma(e, __builtin_fma((double)t, s, a.ws_sums[2 * (u0 + c) + 1]), sum_t);
+    }
+    sum = wave_reduce(sum, AddOp{});
+    sum_t = wave_reduce(sum_t, AddOp{});
+    put(red_sum, sum);
+    put(red_t, sum_t);
+    __syncthreads();
+    sum = sum_of(m, joined(red_sum, sum, AddOp{}));
+    sum_t = joined(red_t, sum_t, AddOp{});
     const double L = log(sum);
-    if (threadIdx.x == 0) write_stats(a, i, m, sum, sum_z, L);
+    if (threadIdx.x == 0) write_stats(a, i, m, sum, sum_t, L);
     for (int p = threadIdx.x; p < a.P; p += T) {
+        if (p >= T) tc = target_of<E>(a, i, p, tx);
         uint32_t n = 0;
-        if (a.rank)
+        if (a.rank) {
+#pragma unroll 8
             for (int c = 0; c < a.chunks; ++c) n += a.ws_rank[(u0 + c) * a.P + p];
-        write_target<E>(a, i, p, n, m, L);
+        }
+        write_target(a, i, p, tc, tx, n, m, L);
     }
     if (a.K == 0) return;
 
-    uint32_t total = 0;
-    for (int c = threadIdx.x; c < a.chunks; c += T) total += a.ws_count[u0 + c];
-    total = block_reduce<T>(total, red_key, AddOp{});
-    auto each = [&](auto f) {
-        for (int c = threadIdx.x >> 6; c < a.chunks; c += T / 64) {
-            const int n = (int)a.ws_count[u0 + c];
-            for (int e = lane_id(); e < n; e += 64) f(a.ws_cand[(u0 + c) * a.cap + e]);
-        }
-    };
-    uint64_t bound = 0;
-    if (total > (uint32_t)a.cap) {
-        uint64_t least = ~(uint64_t)0;
-        each([&](uint64_t o) { least = o < least ? o : least; });
-        __shared__ uint64_t red_o[4];
-        least = ~block_reduce<T>(~least, red_o, MaxOp{});
-        bound = select_bound<T>(each, (uint32_t)a.K, (uint32_t)a.cap, least, order_of(top, 0, a.cbits), hist);
-    }
-    if (threadIdx.x == 0) counter = 0;
-    __syncthreads();
-    each([&](uint64_t o) {
-        if (o >= bound) {
-            const uint32_t at = atomicAdd(&counter, 1u);
-            if (at < (uint32_t)a.cap) cand[at] = o;
-        }
-    });
-    __syncthreads();
-    write_best<T>(a, i, cand, (int)counter, m, L);
+    have = joined(red_have, have, AddOp{});
+    least = joined(red_least, least, MinOp{});
+    const uint32_t n = in_registers
+        ? pick<T>(Numbers<kJoinHeld>{o, a.cbits}, (int)have, least, key_of(m), a, cand, hist, &counter)
+        : pick<T>(Far{from, total, T, a.cbits}, (int)have, least, key_of(m), a, cand, hist, &counter);
+    write_best<T>(a, i, cand, (int)n, m, L);
 }
 
 // ---------------------------------------------------------------------------
@@ -493,19 +651,19 @@ __device__ __forceinline__ void store_columns(void* dX, int64_t at, int n, const
     }
 }
 
-template <int E, int T>
+template <int E, int T, int N>
 __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
 {
-    typedef Layout<E, T> Y;
+    typedef Layout<E, T, N> Y;
     __shared__ float add[Y::kColumns];  // the targets' gradients, by column
     __shared__ int cols[T];
     __shared__ float grads[T];
-    __shared__ float red[4];
+    __shared__ float red[T / 64];
 
     const int64_t unit = blockIdx.x, i = unit / a.chunks;
     const int c0 = (int)(unit % a.chunks) * Y::kColumns;
-    float x[kLpValues];
-    load_columns<E, T>(a, i, c0, x);
+    float x[N];
+    load_columns<E, T, N>(a, i, c0, x);
     for (int k = threadIdx.x; k < Y::kColumns; k += T) add[k] = 0.0f;
     float G = 0.0f;
     for (int p0 = 0; p0 < a.P; p0 += T) {
@@ -538,14 +696,16 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
             }
         }
     }
-    G = block_reduce<T>(G, red, AddOp{});
+    G = wave_reduce(G, AddOp{});
+    put(red, G);
     __syncthreads();
+    G = joined(red, G, AddOp{});
 
     const float m = a.norm_in[2 * i], L = a.norm_in[2 * i + 1];
     const float gh = a.g_entropy ? a.g_entropy[i] : 0.0f, H = a.g_entropy ? a.entropy_in[i] : 0.0f;
     const int n = a.Nd - c0;
 #pragma unroll
-    for (int g = 0; g < kLpValues / Y::V; ++g) {
+    for (int g = 0; g < N / Y::V; ++g) {
         const int at = Y::place(g * Y::V);
         float y[Y::V];
 #pragma unroll
@@ -564,24 +724,30 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
     }
 }
 
+// Rows of up to 1024 columns take one wave, with as few columns a thread as one load
+// brings where that is enough.
 template <int E>
 void forward(const LogprobArgs& a, hipStream_t stream)
 {
-    if (a.Nd <= 64 * kLpValues) {
-        hipLaunchKernelGGL((logprob_part_kernel<E, 64, true>), dim3((unsigned)a.Nq), dim3(64), 0, stream, a);
-    } else if (a.chunks == 1) {
-        hipLaunchKernelGGL((logprob_part_kernel<E, 256, true>), dim3((unsigned)a.Nq), dim3(256), 0, stream, a);
-    } else {
-        hipLaunchKernelGGL((logprob_part_kernel<E, 256, false>), dim3((unsigned)(a.Nq * a.chunks)), dim3(256), 0, stream, a);
-        hipLaunchKernelGGL((logprob_join_kernel<E>), dim3((unsigned)a.Nq), dim3(256), 0, stream, a);
+    constexpr int V = Layout<E, 64, kLpValues>::V;
+    const dim3 rows((unsigned)a.Nq), chunks((unsigned)(a.Nq * a.chunks));
+    if (a.Nd <= 64 * V) hipLaunchKernelGGL((logprob_part_kernel<E, 64, V, true>), rows, dim3(64), 0, stream, a);
+    else if (a.Nd <= 64 * kLpValues) hipLaunchKernelGGL((logprob_part_kernel<E, 64, kLpValues, true>), rows, dim3(64), 0, stream, a);
+    else if (a.chunks == 1) hipLaunchKernelGGL((logprob_part_kernel<E, 256, kLpValues, true>), rows, dim3(256), 0, stream, a);
+    else {
+        hipLaunchKernelGGL((logprob_part_kernel<E, 256, kLpValues, false>), chunks, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((logprob_join_kernel<E>), rows, dim3(kJoinThreads), 0, stream, a);
     }
 }
 
 template <int E>
 void backward(const LogprobArgs& a, hipStream_t stream)
 {
-    if (a.Nd <= 64 * kLpValues) hipLaunchKernelGGL((logprob_bwd_kernel<E, 64>), dim3((unsigned)a.Nq), dim3(64), 0, stream, a);
-    else hipLaunchKernelGGL((logprob_bwd_kernel<E, 256>), dim3((unsigned)(a.Nq * a.chunks)), dim3(256), 0, stream, a);
+    constexpr int V = Layout<E, 64, kLpValues>::V;
+    const dim3 rows((unsigned)a.Nq), chunks((unsigned)(a.Nq * a.chunks));
+    if (a.Nd <= 64 * V) hipLaunchKernelGGL((logprob_bwd_kernel<E, 64, V>), rows, dim3(64), 0, stream, a);
+    else if (a.Nd <= 64 * kLpValues) hipLaunchKernelGGL((logprob_bwd_kernel<E, 64, kLpValues>), rows, dim3(64), 0, stream, a);
+    else hipLaunchKernelGGL((logprob_bwd_kernel<E, 256, kLpValues>), chunks, dim3(256), 0, stream, a);
 }
 
 // A grid's threads stay below 2^32: launches of at most `rows` rows.
@@ -612,7 +778,6 @@ hipError_t by_rows(LogprobArgs a, int64_t es, F once)
             a.ws_sums += 2 * rows * a.chunks;
             a.ws_cand += rows * a.chunks * a.cap;
             a.ws_top += rows * a.chunks;
-            a.ws_count += rows * a.chunks;
             a.ws_rank += rows * a.chunks * a.P;
         }
     }

@@ -23,10 +23,9 @@ struct LogprobArgs {
     int32_t* top_idx;   // [Nq, K]
     float* top_logp;    // [Nq, K]
     // workspace of rows of several chunks: of each (row, chunk)
-    double* ws_sums;    // sum of exp(z), sum of exp(z) z; z against the chunk's largest
-    uint64_t* ws_cand;  // [cap] candidates for the best columns
-    uint32_t* ws_top;   // key of the largest score
-    uint32_t* ws_count; // candidates written
+    double* ws_sums;    // sum of 2^t, sum of 2^t t; t against the chunk's largest
+    uint64_t* ws_cand;  // [cap] candidates for the best columns, 0 behind the last
+    float* ws_top;      // the largest score
     uint32_t* ws_rank;  // [P] candidates before each target
     int32_t chunks;     // of a row
     int32_t cap;        // most candidates that one selection may leave

@@ -35,14 +35,13 @@ int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 
 // Byte offsets of the workspace's parts, and its size.
 struct Parts {
-    int64_t cand, top, count, rank, size;
+    int64_t cand, top, rank, size;
     Parts(int64_t Nq, int64_t Nd, int64_t P, int64_t K)
     {
         const int64_t u = Nq * chunks_of(Nd);
         cand = u * 16;
         top = align16(cand + u * 8 * logprob_cap(K));
-        count = align16(top + u * 4);
-        rank = align16(count + u * 4);
+        rank = align16(top + u * 4);
         size = align16(rank + u * 4 * P);
     }
 };
@@ -93,8 +92,7 @@ maxsim_status_t maxsim_logprob_fwd(maxsim_dtype_t dtype, const void* X, int64_t 
         char* w = (char*)workspace;
         a.ws_sums = (double*)w;
         a.ws_cand = (uint64_t*)(w + at.cand);
-        a.ws_top = (uint32_t*)(w + at.top);
-        a.ws_count = (uint32_t*)(w + at.count);
+        a.ws_top = (float*)(w + at.top);
         a.ws_rank = (uint32_t*)(w + at.rank);
     }
     a.X = X;

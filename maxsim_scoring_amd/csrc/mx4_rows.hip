@@ -9,11 +9,11 @@
 // next to them were compared with the definition, at exponents from -127 to 127).
 // Without normalisation blocks are independent and pass once.
 //
-// With normalisation a row's squares are summed in float64 while the row stays in
-// registers. A code is decided on the quotient x / ||x||, and one that falls on
-// the wrong side of a border is a whole step off, so the float32 quotient (off by
-// less than 2 units in the last place) is used only where it is further than 4
-// from every border; the others are formed again in float64.
+// With normalisation the row stays in registers while its squares are summed. A code
+// is decided on the quotient x / ||x||, and one that falls on the wrong side of a
+// border is a whole step off. So the float32 quotient is used only where it is
+// further from every border than its error can be; a wave that holds another one
+// (one in about 50) sums the squares again in float64 and forms those in float64.
 #include "mx4_common.hpp"
 
 namespace maxsim {
@@ -118,64 +118,31 @@ __device__ __forceinline__ void emit(const Mx4RowArgs& a, int64_t row, int u, co
     put8(a, row, u, convert8(x, e), odd ? kNanScale : e + 127);
 }
 
-// What a normalised row's codes need beside its values.
-struct Norm {
-    double n;   // the norm
-    float r;    // 1 / n
-    bool zero;  // a row of zeros
-    bool odd;   // holds a NaN or an infinity
-    bool far;   // r may be subnormal or infinite: float64 throughout
-};
-__device__ __forceinline__ Norm norm_of(double ss, float top)
-{
-    Norm s;
-    s.odd = !(top <= 0x1.fffffep127f);
-    s.zero = !s.odd && top < kTiny;
-    s.n = s.zero ? 1.0 : __builtin_sqrt(ss);
-    s.r = (float)(1.0 / s.n);
-    s.far = !(s.n > 0x1p-100 && s.n < 0x1p100);
-    return s;
-}
-
-// The border between codes lies at magnitudes whose fraction is a multiple of a
-// quarter, as do the powers of two: is v within 4 units in the last place of one?
-__device__ __forceinline__ bool near_border(float v)
-{
-    return ((__builtin_bit_cast(uint32_t, v) + 4u) & 0x1fffffu) < 8u;
-}
-
+// The code of v / 2^e, v not NaN.
 __device__ __forceinline__ uint32_t code_of(double v, int e)
 {
     const double m = __builtin_ldexp(__builtin_fabs(v), -e);
     const uint32_t c = (uint32_t)(m > 0.25) + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0);
     return c | (__builtin_signbit(v) ? 8u : 0u);
 }
-
-__device__ __forceinline__ void emit_norm(const Mx4RowArgs& a, int64_t row, int u, const float (&x)[8], const Norm& s)
+// Codes of 8 values over the norm n, and their block's exponent, from its largest
+// magnitude m > 0.
+__device__ __forceinline__ uint32_t exact8(const float (&x)[8], double n, float m, int& e)
 {
-    const float m = quad_max(max8(x));
-    float v[8];
-    const float vm = m * s.r;
-    bool slow = s.far;
+    e = clamp_exp((int)(__builtin_bit_cast(uint64_t, (double)m / n) >> 52) - 1023 - 2);
+    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = s.zero ? 0.0f : x[i] * s.r;
-        slow |= near_border(v[i]) && v[i] != 0.0f;
-    }
-    // every lane of the block takes the same way here: vm is the block's
-    const bool slow_scale = m != 0.0f && (s.far || vm < 0x1p-100f || near_border(vm));
-    int e = s.zero || m == 0.0f ? 0 : clamp_exp(__builtin_amdgcn_frexp_expf(vm) - 3);
-    if (slow_scale && !s.zero) {
-        const double q = (double)m / s.n;
-        e = clamp_exp((int)(__builtin_bit_cast(uint64_t, q) >> 52) - 1023 - 2);
-    }
-    uint32_t w = convert8(v, s.odd ? 0 : e);
-    if ((slow || slow_scale) && !s.zero) {
-        w = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w |= code_of((double)x[i] / s.n, e) << (4 * i);
-    }
-    put8(a, row, u, w, s.odd ? kNanScale : e + 127);
+    for (int i = 0; i < 8; ++i) w |= code_of((double)x[i] / n, e) << (4 * i);
+    return w;
+}
+
+// The borders between codes lie at magnitudes whose fraction is a multiple of a
+// quarter, as do the powers of two: a number below 2 W << 11 where v is within W
+// units in the last place of one.
+template <int W>
+__device__ __forceinline__ uint32_t from_border(float v)
+{
+    return (__builtin_bit_cast(uint32_t, v) + (uint32_t)W) << 11;
 }
 
 template <int E, bool WHOLE>
@@ -199,65 +166,141 @@ __global__ __launch_bounds__(kThreads) void quantize_mx4_kernel(Mx4RowArgs a)
     }
 }
 
-__device__ __forceinline__ double lanes_sum(double v, int lanes)
+// Sum or maximum over the G lanes of a row, the same bits in every lane.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v)
 {
-    for (int m = 1; m < lanes; m *= 2) v += __shfl_xor(v, m, 64);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+template <int G, typename OP>
+__device__ __forceinline__ float lanes_reduce(float v, OP op)
+{
+    v = op(v, dpp_f<0xB1>(v));  // quad_perm [1,0,3,2]
+    v = op(v, dpp_f<0x4E>(v));  // quad_perm [2,3,0,1]
+    if constexpr (G >= 8) v = op(v, dpp_f<0x141>(v));   // row_half_mirror
+    if constexpr (G >= 16) v = op(v, dpp_f<0x140>(v));  // row_mirror
+    if constexpr (G >= 32) v = op(v, shfl_xor_f(v, 16));
+    if constexpr (G >= 64) v = op(v, shfl_xor_f(v, 32));
     return v;
 }
-__device__ __forceinline__ float lanes_max(float v, int lanes)
+template <int G>
+__device__ __forceinline__ double lanes_sum(double v)
 {
-    for (int m = 1; m < lanes; m *= 2) v = __builtin_elementwise_maximum(v, shfl_xor_f(v, m));
+#pragma unroll
+    for (int m = 1; m < G; m *= 2) v += __shfl_xor(v, m, 64);
     return v;
 }
 
-// U units of 8 values a lane stay in registers (0: the row is read twice).
-template <int E, bool WHOLE, int U>
+// G lanes hold a row, U units of 8 values each.
+template <int E, bool WHOLE, int G, int U>
 __global__ __launch_bounds__(kThreads) void quantize_mx4_norm_kernel(Mx4RowArgs a)
 {
-    constexpr int kHeld = U > 0 ? U : 1;
-    const int lanes = 1 << a.log2_lanes, lane = threadIdx.x & (lanes - 1), units = 4 * a.nb;
-    const int rows = kThreads >> a.log2_lanes;
-    for (int64_t row = (int64_t)blockIdx.x * rows + (threadIdx.x >> a.log2_lanes); row < a.T; row += (int64_t)gridDim.x * rows) {
-        if (a.mask && !a.mask[row]) {
-            for (int u = lane; u < units; u += lanes) put8(a, row, u, 0, kZeroScale);
-            continue;
-        }
-        float x[kHeld][8];
-        double ss = 0.0;
-        float top = 0.0f;
-        auto add = [&](const float (&v)[8]) {
-            top = __builtin_elementwise_maximum(top, max8(v));
+    // The sum of squares passes 8 U + 6 additions, each off by 2^-24 of it, and its root
+    // half of that; the root, its reciprocal and the product add less than 4 units. A
+    // unit in the last place is at least 2^-24 of the value.
+    constexpr int W = 8 * U + 16;
+    const int lane = threadIdx.x & (G - 1), units = 4 * a.nb;
+    constexpr int rows = kThreads / G;
+    for (int64_t row = (int64_t)blockIdx.x * rows + threadIdx.x / G; row < a.T; row += (int64_t)gridDim.x * rows) {
+        const bool live = !a.mask || a.mask[row];
+        float x[U][8];
+        float ss = 0.0f, top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)v[i], (double)v[i], ss);
-        };
-        if constexpr (U > 0) {
+        for (int j = 0; j < U; ++j) {
+            if (live && lane + j * G < units) load8<E, WHOLE>(a.X, row, a.d, 8 * (lane + j * G), x[j]);
+            else {
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (lane + j * lanes < units) load8<E, WHOLE>(a.X, row, a.d, 8 * (lane + j * lanes), x[j]);
-                else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[j][i] = 0.0f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < U; ++j) add(x[j]);
-        } else {
-#pragma unroll 4
-            for (int u = lane; u < units; u += lanes) {
-                load8<E, WHOLE>(a.X, row, a.d, 8 * u, x[0]);
-                add(x[0]);
+                for (int i = 0; i < 8; ++i) x[j][i] = 0.0f;
             }
         }
-        const Norm s = norm_of(lanes_sum(ss, lanes), lanes_max(top, lanes));
-        if constexpr (U > 0) {
+        float m[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            m[j] = quad_max(max8(x[j]));
+            top = __builtin_elementwise_maximum(top, m[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(x[j][i], x[j][i], ss);
+        }
+        ss = lanes_reduce<G>(ss, [](float p, float q) { return p + q; });
+        top = lanes_reduce<G>(top, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
+        const bool odd = !(top <= 0x1.fffffep127f), zero = !odd && top < kTiny;
+        const bool far = !zero && !odd && !(ss > 0x1p-100f && ss < 0x1p100f);
+        const float r = zero || far ? 0.0f : rsqrt_f(ss);
+        uint32_t w[U], redo = 0;
+        int e[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            float v[8];
+            uint32_t near = 0xffffffffu;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = x[j][i] * r;
+                const uint32_t b = from_border<W>(v[i]);
+                near = b < near ? b : near;
+            }
+            const float vm = m[j] * r;  // the block's: every lane of it has the same
+            e[j] = m[j] == 0.0f || zero || odd ? 0 : clamp_exp(__builtin_amdgcn_frexp_expf(vm) - 3);
+            w[j] = convert8(v, e[j]);
+            const bool small = vm < 0x1p-100f;
+            if (near < (uint32_t)(2 * W) << 11 || small || far) {
+                bool again = small || far || from_border<W>(vm) < (uint32_t)(2 * W) << 11;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)  // zeros are nowhere near a border
+                    again |= from_border<W>(v[i]) < (uint32_t)(2 * W) << 11 && v[i] != 0.0f;
+                if (again && m[j] != 0.0f && !zero && !odd) redo |= 1u << j;
+            }
+            // the block's exponent changes in all its lanes or in none
+            const bool again_scale = (small || far || from_border<W>(vm) < (uint32_t)(2 * W) << 11) && m[j] != 0.0f && !zero && !odd;
+            if (again_scale) redo |= 1u << j;
+        }
+        if (__any(redo != 0)) {
+            double s64 = 0.0;
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (lane + j * lanes < units) emit_norm(a, row, lane + j * lanes, x[j], s);
-        } else {
-            for (int u = lane; u < units; u += lanes) {
-                load8<E, WHOLE>(a.X, row, a.d, 8 * u, x[0]);
-                emit_norm(a, row, u, x[0], s);
-            }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s64 = __builtin_fma((double)x[j][i], (double)x[j][i], s64);
+            const double n = __builtin_sqrt(lanes_sum<G>(s64));
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if ((redo >> j) & 1) w[j] = exact8(x[j], n, m[j], e[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (lane + j * G < units) put8(a, row, lane + j * G, w[j], odd ? kNanScale : e[j] + 127);
+    }
+}
+
+// Rows longer than the registers hold: one wave per row, read twice, in float64
+// throughout.
+template <int E, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void quantize_mx4_norm_long_kernel(Mx4RowArgs a)
+{
+    const int lane = threadIdx.x & 63, units = 4 * a.nb;
+    constexpr int rows = kThreads / 64;
+    for (int64_t row = (int64_t)blockIdx.x * rows + threadIdx.x / 64; row < a.T; row += (int64_t)gridDim.x * rows) {
+        if (a.mask && !a.mask[row]) {
+            for (int u = lane; u < units; u += 64) put8(a, row, u, 0, kZeroScale);
+            continue;
+        }
+        float x[8], top = 0.0f;
+        double ss = 0.0;
+#pragma unroll 4
+        for (int u = lane; u < units; u += 64) {
+            load8<E, WHOLE>(a.X, row, a.d, 8 * u, x);
+            top = __builtin_elementwise_maximum(top, max8(x));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = __builtin_fma((double)x[i], (double)x[i], ss);
+        }
+        top = lanes_reduce<64>(top, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
+        const double n = __builtin_sqrt(lanes_sum<64>(ss));
+        const bool odd = !(top <= 0x1.fffffep127f), zero = !odd && top < kTiny;
+        for (int u = lane; u < units; u += 64) {
+            load8<E, WHOLE>(a.X, row, a.d, 8 * u, x);
+            const float m = quad_max(max8(x));
+            int e = 0;
+            uint32_t w = 0;
+            if (!odd && !zero && m != 0.0f) w = exact8(x, n, m, e);
+            put8(a, row, u, w, odd ? kNanScale : e + 127);
         }
     }
 }
@@ -331,12 +374,18 @@ template <int E, bool WHOLE>
 void quantize(const Mx4RowArgs& a, bool normalize, hipStream_t stream)
 {
     const dim3 grid = row_grid(a), block(kThreads);
-    const int per_lane = (4 * a.nb + (1 << a.log2_lanes) - 1) >> a.log2_lanes;
+    const int units = 4 * a.nb;
+#define MAXSIM_MX4_NORM(G, U) hipLaunchKernelGGL((quantize_mx4_norm_kernel<E, WHOLE, G, U>), grid, block, 0, stream, a)
     if (!normalize) hipLaunchKernelGGL((quantize_mx4_kernel<E, WHOLE>), grid, block, 0, stream, a);
-    else if (per_lane <= 2) hipLaunchKernelGGL((quantize_mx4_norm_kernel<E, WHOLE, 2>), grid, block, 0, stream, a);
-    else if (per_lane <= 4) hipLaunchKernelGGL((quantize_mx4_norm_kernel<E, WHOLE, 4>), grid, block, 0, stream, a);
-    else if (per_lane <= 8) hipLaunchKernelGGL((quantize_mx4_norm_kernel<E, WHOLE, 8>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((quantize_mx4_norm_kernel<E, WHOLE, 0>), grid, block, 0, stream, a);
+    else if (units <= 8) MAXSIM_MX4_NORM(4, 2);
+    else if (units <= 16) MAXSIM_MX4_NORM(8, 2);
+    else if (units <= 32) MAXSIM_MX4_NORM(16, 2);
+    else if (units <= 64) MAXSIM_MX4_NORM(32, 2);
+    else if (units <= 128) MAXSIM_MX4_NORM(64, 2);
+    else if (units <= 256) MAXSIM_MX4_NORM(64, 4);
+    else if (units <= 512) MAXSIM_MX4_NORM(64, 8);
+    else hipLaunchKernelGGL((quantize_mx4_norm_long_kernel<E, WHOLE>), grid, block, 0, stream, a);
+#undef MAXSIM_MX4_NORM
 }
 
 }  // namespace
