@@ -125,15 +125,10 @@ __device__ __forceinline__ uint32_t code_of(double v, int e)
     const uint32_t c = (uint32_t)(m > 0.25) + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0);
     return c | (__builtin_signbit(v) ? 8u : 0u);
 }
-// Codes of 8 values over the norm n, and their block's exponent, from its largest
-// magnitude m > 0.
-__device__ __forceinline__ uint32_t exact8(const float (&x)[8], double n, float m, int& e)
+// The exponent of a block of largest magnitude m > 0 over the norm n.
+__device__ __forceinline__ int exact_exp(double n, float m)
 {
-    e = clamp_exp((int)(__builtin_bit_cast(uint64_t, (double)m / n) >> 52) - 1023 - 2);
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w |= code_of((double)x[i] / n, e) << (4 * i);
-    return w;
+    return clamp_exp((int)(__builtin_bit_cast(uint64_t, (double)m / n) >> 52) - 1023 - 2);
 }
 
 // The borders between codes lie at magnitudes whose fraction is a multiple of a
@@ -195,16 +190,22 @@ __device__ __forceinline__ double lanes_sum(double v)
 template <int E, bool WHOLE, int G, int U>
 __global__ __launch_bounds__(kThreads) void quantize_mx4_norm_kernel(Mx4RowArgs a)
 {
-    // The sum of squares passes 8 U + 6 additions, each off by 2^-24 of it, and its root
-    // half of that; the root, its reciprocal and the product add less than 4 units. A
-    // unit in the last place is at least 2^-24 of the value.
-    constexpr int W = 8 * U + 16;
+    // A square passes 2 U + 8 additions (four sums in a lane, 64 lanes at most), each off
+    // by 2^-24 of the sum, and the root by half of that; the root, its reciprocal and
+    // the product add less than 4 units. A unit in the last place is at least 2^-24 of
+    // the value.
+    constexpr int W = U + 12;
     const int lane = threadIdx.x & (G - 1), units = 4 * a.nb;
     constexpr int rows = kThreads / G;
     for (int64_t row = (int64_t)blockIdx.x * rows + threadIdx.x / G; row < a.T; row += (int64_t)gridDim.x * rows) {
         const bool live = !a.mask || a.mask[row];
-        float x[U][8];
-        float ss = 0.0f, top = 0.0f;
+        if (!__any(live)) {  // the end of a padded document
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (lane + j * G < units) put8(a, row, lane + j * G, 0, kZeroScale);
+            continue;
+        }
+        float x[U][8], part[4] = {0.0f, 0.0f, 0.0f, 0.0f}, top = 0.0f;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (live && lane + j * G < units) load8<E, WHOLE>(a.X, row, a.d, 8 * (lane + j * G), x[j]);
@@ -219,50 +220,75 @@ __global__ __launch_bounds__(kThreads) void quantize_mx4_norm_kernel(Mx4RowArgs 
             m[j] = quad_max(max8(x[j]));
             top = __builtin_elementwise_maximum(top, m[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(x[j][i], x[j][i], ss);
+            for (int i = 0; i < 8; ++i) part[i & 3] = __builtin_fmaf(x[j][i], x[j][i], part[i & 3]);
         }
-        ss = lanes_reduce<G>(ss, [](float p, float q) { return p + q; });
+        const float ss = lanes_reduce<G>((part[0] + part[1]) + (part[2] + part[3]), [](float p, float q) { return p + q; });
         top = lanes_reduce<G>(top, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
         const bool odd = !(top <= 0x1.fffffep127f), zero = !odd && top < kTiny;
         const bool far = !zero && !odd && !(ss > 0x1p-100f && ss < 0x1p100f);
         const float r = zero || far ? 0.0f : rsqrt_f(ss);
-        uint32_t w[U], redo = 0;
+        constexpr uint32_t kNear = (uint32_t)(2 * W) << 11;
+        uint32_t w[U], near = 0xffffffffu;
         int e[U];
+        bool small = far;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             float v[8];
-            uint32_t near = 0xffffffffu;
+            uint32_t least = 0xffffffffu;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[i] = x[j][i] * r;
                 const uint32_t b = from_border<W>(v[i]);
-                near = b < near ? b : near;
+                least = b < least ? b : least;
             }
-            const float vm = m[j] * r;  // the block's: every lane of it has the same
-            e[j] = m[j] == 0.0f || zero || odd ? 0 : clamp_exp(__builtin_amdgcn_frexp_expf(vm) - 3);
+            if (least < kNear) {  // zeros look like borders
+                least = 0xffffffffu;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t b = v[i] != 0.0f ? from_border<W>(v[i]) : 0xffffffffu;
+                    least = b < least ? b : least;
+                }
+            }
+            near = least < near ? least : near;
+            const float vm = m[j] * r;
+            // frexp's exponent of 0 is 0 too: blocks of zeros have e = 0
+            e[j] = vm == 0.0f ? 0 : clamp_exp(__builtin_amdgcn_frexp_expf(vm) - 3);
             w[j] = convert8(v, e[j]);
-            const bool small = vm < 0x1p-100f;
-            if (near < (uint32_t)(2 * W) << 11 || small || far) {
-                bool again = small || far || from_border<W>(vm) < (uint32_t)(2 * W) << 11;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)  // zeros are nowhere near a border
-                    again |= from_border<W>(v[i]) < (uint32_t)(2 * W) << 11 && v[i] != 0.0f;
-                if (again && m[j] != 0.0f && !zero && !odd) redo |= 1u << j;
-            }
-            // the block's exponent changes in all its lanes or in none
-            const bool again_scale = (small || far || from_border<W>(vm) < (uint32_t)(2 * W) << 11) && m[j] != 0.0f && !zero && !odd;
-            if (again_scale) redo |= 1u << j;
+            small |= vm < 0x1p-100f && m[j] != 0.0f;
         }
-        if (__any(redo != 0)) {
+        if (__any((near < kNear || small) && !zero && !odd)) {
+            // the row is read again, so that it need not stay in registers until here
+            auto again = [&](int j, float (&y)[8]) {
+                const int u = lane + j * G;
+                load8<E, WHOLE>(a.X, row, a.d, u < units ? 8 * u : 0, y);
+                if (!live || u >= units) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+                }
+            };
             double s64 = 0.0;
+#pragma unroll 1
+            for (int j = 0; j < U; ++j) {
+                float y[8];
+                again(j, y);
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s64 = __builtin_fma((double)x[j][i], (double)x[j][i], s64);
+                for (int i = 0; i < 8; ++i) s64 = __builtin_fma((double)y[i], (double)y[i], s64);
+            }
             const double n = __builtin_sqrt(lanes_sum<G>(s64));
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-                if ((redo >> j) & 1) w[j] = exact8(x[j], n, m[j], e[j]);
+            for (int j = 0; j < U; ++j) {
+                float y[8];
+                again(j, y);
+                // a block's exponent is formed again in all its lanes or in none, with all its
+                // codes; otherwise single codes are
+                const float m = quad_max(max8(y));
+                const bool some = m != 0.0f && !zero && !odd, all = some && (small || from_border<W>(m * r) < kNear);
+                if (all) e[j] = exact_exp(n, m);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (all || (some && from_border<W>(y[i] * r) < kNear && y[i] != 0.0f))
+                        w[j] = (w[j] & ~(15u << (4 * i))) | code_of((double)y[i] / n, e[j]) << (4 * i);
+            }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j)
@@ -299,7 +325,11 @@ __global__ __launch_bounds__(kThreads) void quantize_mx4_norm_long_kernel(Mx4Row
             const float m = quad_max(max8(x));
             int e = 0;
             uint32_t w = 0;
-            if (!odd && !zero && m != 0.0f) w = exact8(x, n, m, e);
+            if (!odd && !zero && m != 0.0f) {
+                e = exact_exp(n, m);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w |= code_of((double)x[i] / n, e) << (4 * i);
+            }
             put8(a, row, u, w, odd ? kNanScale : e + 127);
         }
     }
