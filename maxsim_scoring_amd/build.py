@@ -34,7 +34,7 @@ FLAGS = [
 
 
 # Per-source additions. The Chamfer kernel's MFMA results feed VALU min
-# updates directly, so they go to ordinary VGPRs instead of the
+# updates directly (those of the 4-bit scores max updates), so they go to ordinary VGPRs instead of the
 # accumulation registers (no copy back per MFMA); the other kernels keep the
 # compiler's default register form. The embedding head carries activations and
 # gradients, where an overflow upstream must stay visible: NaNs are honoured
@@ -44,7 +44,7 @@ FLAGS = [
 _NANS = ["-Xarch_device", "-fhonor-nans", "-Xarch_device", "-mamdgpu-ieee"]
 EXTRA = {"chamfer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "topk.hip": _NANS, "embed_rows.hip": _NANS, "embed_linear.hip": _NANS,
-         "mx4_rows.hip": _NANS, "mx4_linear.hip": _NANS, "fwd_mx4.hip": _NANS, "logprob.hip": _NANS}
+         "mx4_rows.hip": _NANS, "mx4_linear.hip": _NANS, "fwd_mx4.hip": _NANS + ["-mllvm", "-amdgpu-mfma-vgpr-form"], "logprob.hip": _NANS}
 
 
 def _run(cmd, verbose):
