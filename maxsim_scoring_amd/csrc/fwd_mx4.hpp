@@ -1,0 +1,392 @@
+#pragma once
+
+// Cross-product MaxSim of microscaled 4-bit queries and documents for gfx950,
+// with masks, optional argmax and queries of any length.
+//
+//   score[i,j] = sum_s max_t sum_b 2^(eq[s,b] + ed[t,b]) <Q[s,b], D[t,b]>
+//
+// The tile is transposed as in the other forwards, S^T = D . Q^T: MFMA rows are
+// document tokens, columns query tokens, so the max over tokens stays inside a
+// lane until the document ends. The block-scaled MFMA takes codes and exponents as
+// they are stored; a token of 128 channels is 64 bytes of codes and one word of
+// exponents, of which lane half h takes blocks 2 h and 2 h + 1 of every four.
+//
+// A unit of work is one wave: up to NTW tiles of 32 query tokens, held in
+// registers, against a range of documents, whose tokens go straight from memory
+// to registers, P tiles of 32 ahead and across the ends of documents. The tokens of a
+// unit stay in the caches for the other units of its range, which follow it on the
+// same XCD. Queries of more than NTW tiles are split over the four waves of a
+// workgroup, which leave their sums in LDS to be added in order; otherwise waves share
+// nothing.
+//
+// Masked tokens cost nothing per query tile: their codes and exponents are
+// replaced by zeros and 2^0 (so that a NaN among them is not seen) and the
+// accumulator starts at -inf in their rows. A range's mask becomes bits in LDS
+// first, so that the masked tail of a padded document is not read at all.
+#include "mx4_common.hpp"
+#include "kernels.hpp"
+
+namespace maxsim {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kMaskWords = 512;  // of a wave: the bits of 16,384 tokens
+constexpr int kSplitDocs = 256;  // documents whose sums the waves of a split query leave in LDS
+
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
+
+// One bit for each of the 4 bytes of x that is not 0.
+__device__ __forceinline__ uint32_t byte_bits(uint32_t x)
+{
+    x |= x >> 4;
+    x |= x >> 2;
+    x |= x >> 1;
+    return (((x & 0x01010101u) * 0x01020408u) >> 24) & 0xfu;
+}
+
+// Bits of mask bytes p[0 .. n - 1], n <= 32.
+__device__ __forceinline__ uint32_t mask_word(const uint8_t* p, int n)
+{
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (4 * k + 4 <= n) bits |= byte_bits(*(const u32_any*)(p + 4 * k)) << (4 * k);
+    for (int i = n & ~3; i < n; ++i) bits |= (uint32_t)(p[i] != 0) << i;
+    return bits;
+}
+
+__device__ __forceinline__ float vmax(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// The largest of 16 values and m, NaN where one is.
+__device__ __forceinline__ float max16(const f32x16& v, float m)
+{
+#pragma unroll
+    for (int q = 0; q < 16; q += 2) m = vmax(vmax(m, v[q]), v[q + 1]);
+    return m;
+}
+
+// 4 G blocks of one token of this lane's half: blocks 4 g + 2 h + k in code[2 g + k],
+// exponents in bytes 0 and 1 of scale[g].
+template <int G>
+struct Token {
+    i32x4 code[2 * G];
+    int scale[G];
+};
+
+// FAST: nb is 4 G and the exponents of a token are aligned words.
+// base, sbase: the first token of the tile (uniform); row: this lane's. Blocks behind
+// the last one repeat it with exponent 2^0: QUERY makes their codes zeros, so that
+// they add nothing, whatever the document's are.
+template <int G, bool FAST, bool QUERY>
+__device__ __forceinline__ void load_token(Token<G>& t, const uint8_t* base, const uint8_t* sbase, int row, int h, int nb)
+{
+    const uint32_t at = (uint32_t)(row * nb) * 16, sat = (uint32_t)(row * nb);
+    static_for<0, G>([&](auto g) {
+        if constexpr (FAST) {
+            t.code[2 * g] = *(const i32x4*)(base + (at + (4 * g + 2 * h) * 16));
+            t.code[2 * g + 1] = *(const i32x4*)(base + (at + (4 * g + 2 * h + 1) * 16));
+            t.scale[g] = *(const int*)(sbase + (sat + 4 * g));
+        } else {
+            const int b = 4 * g + 2 * h;  // and b + 1
+            static_for<0, 2>([&](auto k) {
+                const int c = b + k < nb ? b + k : nb - 1;
+                t.code[2 * g + k] = *(const i32x4*)(base + (at + c * 16));
+                if (QUERY) t.code[2 * g + k] = b + k < nb ? t.code[2 * g + k] : i32x4{};
+            });
+            // both exponents in one load: that of a last block alone comes with the one before
+            uint32_t s;
+            if (nb == 1) s = sbase[sat];
+            else {
+                const int c = b < nb - 2 ? b : nb - 2;
+                s = *(const u16_any*)(sbase + (sat + c));
+                s >>= b == nb - 1 ? 8 : 0;
+            }
+            s = b + 1 < nb ? s : b < nb ? (s & 0xffu) | 0x7f00u : 0x7f7fu;
+            t.scale[g] = (int)s;
+        }
+    });
+}
+// The exponents of this lane's half moved to the low bytes.
+template <int G, bool FAST>
+__device__ __forceinline__ void place_scales(Token<G>& t, int h)
+{
+    if constexpr (FAST) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) t.scale[g] = (int)((uint32_t)t.scale[g] >> (16 * h));
+    }
+}
+
+template <int G, int NTW, int P, bool ARGMAX, bool FAST, bool SPLIT>
+__global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
+{
+    __shared__ uint32_t mask_lds[kWaves][kMaskWords];
+    __shared__ float part[SPLIT ? kWaves : 1][SPLIT ? kSplitDocs : 1];
+
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id(), col = lane & 31, h = lane >> 5;
+    uint32_t* const my_mask = mask_lds[wave];
+
+    // unit of work: XCD-aware order (workgroup b runs on XCD b % 8)
+    const int nblk = gridDim.x, b = blockIdx.x;
+    const int full = nblk >> 3, rem = nblk & 7, xcd = b & 7;
+    const int wg = xcd * full + (xcd < rem ? xcd : rem) + (b >> 3);
+    const int64_t unit = SPLIT ? wg : (int64_t)wg * kWaves + wave;
+    if (unit >= (int64_t)a.nqb * a.nranges) return;  // (the whole workgroup, if SPLIT)
+    const int qb = (int)(unit % a.nqb);
+    const int64_t r = unit / a.nqb;
+    const int d0 = uniform((int)(r * a.Nd / a.nranges)), d1 = uniform((int)((r + 1) * a.Nd / a.nranges));
+    if (d0 >= d1) return;
+
+    const int Lq = (int)a.Lq, Ld = (int)a.Ld, nb = a.nb;
+    const int tiles = (Ld + 31) / 32;  // of a document
+    const bool in_lds = a.d_mask && tiles <= kMaskWords;
+    int batch = in_lds ? kMaskWords / tiles : 0x7fffffff;  // documents whose mask LDS holds
+    if (SPLIT) batch = batch < kSplitDocs ? batch : kSplitDocs;
+    // queries of this unit; tiles of one
+    const int i0 = uniform(qb * a.qpw);
+    const int nq = uniform((int)(a.Nq - i0 < a.qpw ? a.Nq - i0 : a.qpw));
+    const int ntq = a.ntq;
+
+    // a split query takes a pass for each kWaves * NTW of its tiles
+    for (int q0 = 0; q0 == 0 || (SPLIT && q0 < ntq); q0 += kWaves * NTW) {
+        const int first = SPLIT ? q0 + wave * NTW : 0;  // this wave's first tile of a split query
+        // ---- the unit's query tiles --------------------------------------------
+        Token<G> q[NTW];
+        uint32_t live = 0;  // bit n: this lane's column of tile n exists and counts
+        static_for<0, NTW>([&](auto n) {
+            // tile n is tile n % ntq of query n / ntq, or tile first + n of the one query
+            const int qi = SPLIT ? 0 : n / ntq, qt = SPLIT ? first + n : n % ntq;
+            const bool tile_in = qi < nq && qt < ntq;
+            const int64_t i = i0 + (tile_in ? qi : 0);
+            const int t0 = tile_in ? qt * 32 : 0, s = t0 + col;
+            const int row = s < Lq ? col : Lq - 1 - t0;
+            const int64_t tok = i * Lq + t0;
+            load_token<G, FAST, true>(q[n], a.Q + tok * nb * 16, a.q_scale + tok * nb, row, h, nb);
+            place_scales<G, FAST>(q[n], h);
+            const bool on = tile_in && s < Lq && (!a.q_mask || a.q_mask[i * Lq + s]);
+            live |= (uint32_t)on << n;
+        });
+
+        float m[NTW];
+        int best[ARGMAX ? NTW : 1];
+        auto reset = [&] {
+#pragma unroll
+            for (int n = 0; n < NTW; ++n) {
+                m[n] = -__builtin_inff();
+                if (ARGMAX) best[n] = 0;
+            }
+        };
+        reset();
+        bool any = false;  // a token of the document counts
+
+        for (int64_t first_doc = d0; first_doc < d1; first_doc += batch) {
+            const int b0 = (int)first_doc, b1 = d1 - b0 < batch ? d1 : b0 + batch;
+            if (in_lds) {
+                const int words = (b1 - b0) * tiles;
+                for (int w = lane; w < words; w += 64) {
+                    const int64_t doc = b0 + w / tiles;
+                    const int t0 = w % tiles * 32;
+                    my_mask[w] = mask_word(a.d_mask + doc * Ld + t0, Ld - t0 < 32 ? Ld - t0 : 32);
+                }
+                lds_fence();
+                __builtin_amdgcn_wave_barrier();
+            }
+
+            // Sums of a finished document, tile by tile in order.
+            auto finish = [&](int doc) {
+                float sum = 0.0f;
+                int i = i0, at = 0;  // the query of tile n, and which of its tiles that is
+                static_for<0, NTW>([&](auto n) {
+                    if (!SPLIT && i >= i0 + nq) return;
+                    if (SPLIT && first + n >= ntq) return;
+                    float v = m[n];
+                    const float o = shfl_xor_f(v, 32);
+                    if constexpr (ARGMAX) {
+                        const int oi = shfl_xor_i(best[n], 32);
+                        const int idx = o > v || (o == v && oi < best[n]) ? oi : best[n];
+                        const int s = (SPLIT ? first + n : at) * 32 + col;
+                        if (h == 0 && s < Lq) a.argmax[(i * a.Nd + doc) * Lq + s] = idx;
+                    }
+                    v = any && ((live >> n) & 1) ? vmax(v, o) : 0.0f;
+                    sum += lanes0_31_sum(v);
+                    if (!SPLIT && ++at == ntq) {
+                        if (lane == 0) a.scores[i * a.Nd + doc] = sum;
+                        sum = 0.0f;
+                        at = 0;
+                        ++i;
+                    }
+                });
+                if (SPLIT && lane == 0) part[wave][doc - b0] = sum;
+                reset();
+                any = false;
+            };
+
+            // ---- the stream of tiles ---------------------------------------------
+            struct Slot {
+                Token<G> t;
+                uint32_t bits;      // tokens of the tile that count
+                int doc, tile;
+                bool last, valid;   // the document's last tile; there is a tile
+            } slot[P];
+            int doc = b0 - 1, tile = 0, count = 0;  // the tile issued last, tiles of its document
+            uint32_t words = 0;  // this lane's of 64 mask words of doc
+            const uint8_t* codes = a.D + (int64_t)b0 * Ld * nb * 16;  // of the tile issued last
+            const uint8_t* scales = a.d_scale + (int64_t)b0 * Ld * nb;
+            auto issue = [&](Slot& s) {
+                ++tile;
+                codes += 32 * 16 * nb;
+                scales += 32 * nb;
+                if (tile >= count) {  // the next document with a token
+                    for (;;) {
+                        if (++doc >= b1) {
+                            doc = b1;  // stays behind the end; the tile read is the first one's
+                            break;
+                        }
+                        count = tiles;
+                        if (in_lds) {
+                            count = 0;
+                            for (int w0 = 0; w0 < tiles; w0 += 64) {
+                                const uint32_t w = w0 + lane < tiles ? my_mask[(doc - b0) * tiles + w0 + lane] : 0;
+                                const uint64_t some = __ballot(w != 0);
+                                if (some) count = w0 + 64 - __builtin_clzll(some);
+                                if (w0 == 0) words = w;
+                            }
+                        }
+                        if (count > 0) break;
+                        // nothing to score
+                        if constexpr (SPLIT) {
+                            if (lane == 0) part[wave][doc - b0] = 0.0f;
+                        }
+                        for (int i = i0; i < i0 + nq; ++i) {
+                            if (!SPLIT && lane == 0) a.scores[i * a.Nd + doc] = 0.0f;
+                            if (ARGMAX)
+                                for (int e = lane; e < Lq; e += 64) a.argmax[(i * a.Nd + doc) * Lq + e] = 0;
+                        }
+                    }
+                    tile = 0;
+                    if (doc >= b1) count = 0;
+                    const int64_t tok = (int64_t)(doc < b1 ? doc : b0) * Ld;
+                    codes = a.D + tok * nb * 16;
+                    scales = a.d_scale + tok * nb;
+                }
+                s.valid = doc < b1;
+                const int t0 = tile * 32, left = Ld - t0;
+                uint32_t bits = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+                if (in_lds && s.valid) {
+                    if ((tile & 63) == 0 && tile > 0)
+                        words = tile + lane < tiles ? my_mask[(doc - b0) * tiles + tile + lane] : 0;
+                    bits = __builtin_amdgcn_readlane(words, tile & 63);
+                }
+                // rows behind the tile's last token (that counts) repeat it
+                const int last = bits ? 31 - __builtin_clz(bits) : 0;
+                load_token<G, FAST, false>(s.t, codes, scales, col < last ? col : last, h, nb);
+                if (!in_lds && a.d_mask && s.valid)
+                    bits = (uint32_t)__ballot(lane < 32 && lane < left && a.d_mask[(int64_t)doc * Ld + t0 + (lane < left ? lane : 0)]);
+                s.doc = doc;
+                s.tile = tile;
+                s.bits = bits;
+                s.last = tile + 1 == count;
+            };
+            auto consume = [&](Slot& s) {
+                place_scales<G, FAST>(s.t, h);
+                auto fold = [&](auto masked) {
+                    f32x16 start;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) start[e] = 0.0f;
+                    if constexpr (masked) {
+                        const bool on = (s.bits >> col) & 1;
+                        const uint32_t mine = s.bits >> (4 * h);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            start[e] = (mine >> (8 * (e >> 2) + (e & 3))) & 1 ? 0.0f : -__builtin_inff();
+                        // codes are finite whatever they are; an exponent may be NaN
+#pragma unroll
+                        for (int g = 0; g < G; ++g) s.t.scale[g] = on ? s.t.scale[g] : 0;
+                    }
+                    static_for<0, NTW>([&](auto n) {
+                        f32x16 acc = start;
+                        static_for<0, G>([&](auto g) {
+                            acc = mfma32_mx4<0, 0>(s.t.code[2 * g], s.t.scale[g], q[n].code[2 * g], q[n].scale[g], acc);
+                            acc = mfma32_mx4<1, 1>(s.t.code[2 * g + 1], s.t.scale[g], q[n].code[2 * g + 1], q[n].scale[g], acc);
+                        });
+                        if constexpr (!ARGMAX) {
+                            m[n] = max16(acc, m[n]);
+                        } else {
+                            const float top = max16(acc, -__builtin_inff());
+                            if (top > m[n]) {
+                                int row = 0;
+#pragma unroll
+                                for (int e = 15; e >= 0; --e) row = acc[e] == top ? 8 * (e >> 2) + (e & 3) : row;
+                                best[n] = s.tile * 32 + 4 * h + row;
+                            }
+                            m[n] = vmax(m[n], top);
+                        }
+                    });
+                };
+                if (s.bits == 0xffffffffu) fold(std::false_type{});
+                else if (s.bits != 0) fold(std::true_type{});
+                any |= s.bits != 0;
+                if (s.last) finish(s.doc);
+            };
+
+            if (SPLIT && first >= ntq) doc = b1;  // no tile of the query is left for this wave
+            static_for<0, P>([&](auto p) { issue(slot[p]); });
+            while (slot[0].valid) {
+                static_for<0, P>([&](auto p) {
+                    if (slot[p].valid) {
+                        consume(slot[p]);
+                        issue(slot[p]);
+                    }
+                });
+            }
+            if constexpr (SPLIT) {
+                __syncthreads();
+                for (int e = threadIdx.x; e < b1 - b0; e += kWaves * 64) {
+                    float* out = a.scores + (int64_t)i0 * a.Nd + b0 + e;
+                    float sum = part[0][e];
+#pragma unroll
+                    for (int w = 1; w < kWaves; ++w)
+                        if (q0 + w * NTW < ntq) sum += part[w][e];
+                    *out = q0 > 0 ? *out + sum : sum;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+inline int64_t pieces(int64_t n, int b) { return (n + b - 1) / b; }
+
+// WAVES: units that a CU runs at once, 4 for each that a SIMD's registers hold, or
+// fewer where more ran slower.
+template <int G, int NTW, int P, int WAVES>
+void run(Mx4FwdArgs a, hipStream_t stream)
+{
+    const bool split = a.ntq > NTW;
+    a.qpw = split ? 1 : NTW / a.ntq;
+    a.nqb = (int32_t)pieces(a.Nq, a.qpw);
+    const int64_t units = (int64_t)device_cu_count() * (split ? WAVES / kWaves : WAVES);
+    const int64_t want = units / a.nqb > 0 ? units / a.nqb : 1;
+    a.nranges = (int32_t)(want < a.Nd ? want : a.Nd);
+    const int64_t total = (int64_t)a.nqb * a.nranges;
+    const dim3 grid((unsigned)(split ? total : pieces(total, kWaves))), block(kWaves * 64);
+    const bool fast = a.nb == 4 * G && (((uintptr_t)a.q_scale | (uintptr_t)a.d_scale) & 3) == 0;
+    // (more query registers beside an argmax's would spill)
+#define MAXSIM_MX4_SPLIT(ARGMAX, FAST)                                                                                  \
+    do {                                                                                                                \
+        if (split) hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, true>), grid, block, 0, stream, a);      \
+        else hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, false>), grid, block, 0, stream, a);           \
+    } while (0)
+    if constexpr (NTW < 8 && NTW * G < 24) {
+        if (a.argmax && fast) MAXSIM_MX4_SPLIT(true, true);
+        else if (a.argmax) MAXSIM_MX4_SPLIT(true, false);
+    }
+    if (!a.argmax && fast) MAXSIM_MX4_SPLIT(false, true);
+    else if (!a.argmax) MAXSIM_MX4_SPLIT(false, false);
+#undef MAXSIM_MX4_SPLIT
+}
+
+}  // namespace
+
+}  // namespace maxsim

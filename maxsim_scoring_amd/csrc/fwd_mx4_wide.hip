@@ -1,0 +1,26 @@
+// Cross-product MaxSim of microscaled 4-bit queries and documents: the kernels of more
+// than 256 channels.
+#include "fwd_mx4.hpp"
+
+namespace maxsim {
+
+// n: query tiles a wave that leave work for all.
+void launch_fwd_mx4_wide(const Mx4FwdArgs& a, int n, hipStream_t stream)
+{
+    if (a.nb <= 12) {
+        if (n >= 3) run<3, 4, 2, 8>(a, stream);
+        else run<3, 1, 2, 12>(a, stream);
+    } else if (a.nb <= 16) {
+        if (n >= 3) run<4, 4, 2, 8>(a, stream);
+        else run<4, 1, 2, 8>(a, stream);
+    } else if (a.nb <= 24) {
+        if (n >= 3 && !a.argmax) run<6, 4, 2, 4>(a, stream);
+        else if (n >= 2) run<6, 2, 2, 4>(a, stream);
+        else run<6, 1, 2, 8>(a, stream);
+    } else {
+        if (n >= 2) run<8, 2, 2, 4>(a, stream);
+        else run<8, 1, 1, 8>(a, stream);
+    }
+}
+
+}  // namespace maxsim

@@ -56,6 +56,7 @@ hipError_t launch_quantize_mx4(int elem, Mx4RowArgs a, bool normalize, hipStream
 hipError_t launch_dequantize_mx4(Mx4RowArgs a, hipStream_t stream);
 hipError_t launch_linear_mx4(Mx4LinearArgs a, hipStream_t stream);
 hipError_t launch_fwd_mx4(Mx4FwdArgs a, hipStream_t stream);
+void launch_fwd_mx4_wide(const Mx4FwdArgs& a, int n, hipStream_t stream);
 
 // The block-scaled matrix product of 4-bit operands. A lane's 16 bytes are 32
 // codes, one block: lane l of the 32-row form holds row l % 32, block l / 32 of
