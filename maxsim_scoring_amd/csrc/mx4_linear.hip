@@ -22,6 +22,8 @@ namespace maxsim {
 
 namespace {
 
+typedef uint64_t u64_any __attribute__((aligned(1)));
+
 // Writes a wave's NT x 32 channels of TT x 32 tokens, from channel n0 + wn * NT * 32
 // and token t0 + a_row on. ring: LDS of at least 32 x (NT * 32 + 4) floats per
 // wave, free to overwrite.
@@ -79,12 +81,12 @@ __device__ __forceinline__ void store_tile(const Mx4LinearArgs& a, const f32x16 
     }
 }
 
-// Workgroup to tile: consecutive workgroups go to the 8 XCDs in turn, so each XCD
+// Position to tile: consecutive workgroups go to the 8 XCDs in turn, so each XCD
 // takes a contiguous run of tiles, walked in bands of 8 token tiles, whose
 // operands the XCD's L2 then holds.
-__device__ __forceinline__ void tile_of(const Mx4LinearArgs& a, int BT, int BN, int64_t& t0, int& n0)
+__device__ __forceinline__ void tile_of(const Mx4LinearArgs& a, int b, int BT, int BN, int64_t& t0, int& n0)
 {
-    const int nwg = a.tiles_t * a.tiles_n, b = blockIdx.x;
+    const int nwg = a.tiles_t * a.tiles_n;
     const int q = nwg >> 3, r = nwg & 7, x = b & 7;
     const int id = x * q + (x < r ? x : r) + (b >> 3);
     const int per = 8 * a.tiles_n, band = id / per, in = id - band * per;
@@ -104,8 +106,8 @@ struct Tile {
     static constexpr int kCodes = kRows * KB;
     static constexpr int kStage = kCodes + kRows * 8;  // the exponents behind the codes
     static constexpr int kPerWave = kRows / 8 / kWaves;     // wave-wide loads of codes: 8 rows each
-    static constexpr int kScales = kRows / 32 / kWaves;     // and of exponents: 32 rows each
-    static_assert(BT % 32 == 0 && kRows % (32 * kWaves) == 0, "a load stays inside one operand, every wave has as many");
+    static constexpr int kScales = (kRows / 32 + kWaves - 1) / kWaves;  // and of exponents: 32 rows each
+    static_assert(BT % 32 == 0 && BN % 32 == 0 && kRows % (8 * kWaves) == 0, "a load stays inside one operand, every wave has as many");
     static_assert(kWaves * 32 * (NT * 32 + 4) * 4 <= ST * kStage, "the ring holds a turned output");
 };
 
@@ -136,59 +138,60 @@ __device__ __forceinline__ void multiply(const uint8_t* buf, int w_row, int a_ro
 
 // WORDS: the exponents of a row come in aligned words (nb is a multiple of 4) and
 // go to LDS directly; otherwise they pass through registers, byte by byte.
-template <int BT, int BN, int WT, int WN, int ST, bool WORDS>
+// MANY: a workgroup takes every gridDim.x-th tile, and loads the first steps of the
+// next one before it stores the outputs of this one.
+template <int BT, int BN, int WT, int WN, int ST, bool WORDS, bool MANY>
 __global__ __launch_bounds__(WT* WN * 64) void tile_mx4_kernel(Mx4LinearArgs a)
 {
     typedef Tile<BT, BN, WT, WN, ST> C;
     __shared__ __align__(1024) uint8_t ring[ST * C::kStage];
-    __shared__ __align__(16) float bs[BN];
+    __shared__ __align__(16) float bias[2][BN];
 
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int wt = wave / WN, wn = wave % WN;
-
-    int64_t t0;
-    int n0;
-    tile_of(a, BT, BN, t0, n0);
-    const int rows_t = (int)(a.T - t0 < BT ? a.T - t0 : BT);
-    const int rows_n = a.N - n0 < BN ? a.N - n0 : BN;
-    const int row_bytes = a.nb * 16;
-    const uint8_t* A = a.A + t0 * row_bytes;
-    const uint8_t* W = a.W + (int64_t)n0 * row_bytes;
-    const uint8_t* SA = a.a_scale + t0 * a.nb;
-    const uint8_t* SW = a.w_scale + (int64_t)n0 * a.nb;
-    for (int i = threadIdx.x; i < BN; i += C::kThreads) bs[i] = a.bias && i < rows_n ? a.bias[n0 + i] : 0.0f;
-
-    f32x16 acc[C::NT][C::TT];
-#pragma unroll
-    for (int i = 0; i < C::NT; ++i)
-#pragma unroll
-        for (int j = 0; j < C::TT; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     const int a_row = wt * C::TT * 32, w_row = BT + wn * C::NT * 32;
+    const int row_bytes = a.nb * 16, nk = a.nb / 8;  // whole steps
+    const int tiles = a.tiles_t * a.tiles_n;
+    constexpr int L = C::kPerWave + (WORDS ? C::kScales : 0);  // a wave's loads of a step
+    constexpr int S = C::NT * C::TT * 2;                       // stores of a whole tile, at least
 
-    // Which row of its operand a row of the stage holds. Rows past the end of an
-    // operand repeat its last row; what they give is not stored.
-    auto local = [&](int r) {
-        const bool isA = r < BT;
-        const int row = isA ? r : channel_of(r - BT), last = (isA ? rows_t : rows_n) - 1;
-        return row < last ? row : last;
-    };
+    // ---- the tile whose operands are being loaded --------------------------------
+    int64_t t0;
+    int n0, rows_t, rows_n;
+    const uint8_t *A, *W, *SA, *SW;
     // The wave's loads: load j brings 8 rows of codes, one chunk per lane, or (the
     // exponents) 32 rows, one word per lane.
     uint32_t voff[C::kPerWave], soff[C::kScales];
     auto row_of = [&](int j) { return (wave * C::kPerWave + j) * 8; };
-    auto srow_of = [&](int j) { return (wave * C::kScales + j) * 32; };
+    auto srow_of = [&](int j) {  // a spare load repeats the last
+        const int at = (wave * C::kScales + j) * 32;
+        return at < C::kRows ? at : C::kRows - 32;
+    };
+    // Which row of its operand a row of the stage holds. Rows past the end of an
+    // operand repeat its last row; what they give is not stored.
+    auto local = [](int r, int rows_t, int rows_n) {
+        const bool isA = r < BT;
+        const int row = isA ? r : channel_of(r - BT), last = (isA ? rows_t : rows_n) - 1;
+        return row < last ? row : last;
+    };
+    auto enter = [&](int at, float* bs) {
+        tile_of(a, at, BT, BN, t0, n0);
+        rows_t = (int)(a.T - t0 < BT ? a.T - t0 : BT);
+        rows_n = a.N - n0 < BN ? a.N - n0 : BN;
+        A = a.A + t0 * row_bytes;
+        W = a.W + (int64_t)n0 * row_bytes;
+        SA = a.a_scale + t0 * a.nb;
+        SW = a.w_scale + (int64_t)n0 * a.nb;
+        for (int i = threadIdx.x; i < BN; i += C::kThreads) bs[i] = a.bias && i < rows_n ? a.bias[n0 + i] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < C::kPerWave; ++j) {
-        const int r = row_of(j) + lane / 8;
-        voff[j] = (uint32_t)local(r) * (uint32_t)row_bytes + (uint32_t)place<C::KB>(r, lane % 8) * 16;
-    }
+        for (int j = 0; j < C::kPerWave; ++j) {
+            const int r = row_of(j) + lane / 8;
+            voff[j] = (uint32_t)local(r, rows_t, rows_n) * (uint32_t)row_bytes + (uint32_t)place<C::KB>(r, lane % 8) * 16;
+        }
 #pragma unroll
-    for (int j = 0; j < C::kScales; ++j)
-        soff[j] = (uint32_t)local(srow_of(j) + lane / 2) * (uint32_t)a.nb + (uint32_t)(lane & 1) * 4;
-
-    const int nk = a.nb / 8;  // whole steps
+        for (int j = 0; j < C::kScales; ++j)
+            soff[j] = (uint32_t)local(srow_of(j) + lane / 2, rows_t, rows_n) * (uint32_t)a.nb + (uint32_t)(lane & 1) * 4;
+    };
     const uint32_t ring0 = lds_addr(ring);
     auto issue = [&](int i) {
         const uint32_t at = ring0 + (uint32_t)(i % ST) * C::kStage;
@@ -207,55 +210,88 @@ __global__ __launch_bounds__(WT* WN * 64) void tile_mx4_kernel(Mx4LinearArgs a)
             }
         }
     };
-    // Exponents of step i through registers: thread r those of row r; the blocks
-    // behind the last one count as 2^0 (their codes are zeros).
-    static_assert(C::kThreads >= C::kRows, "one row per thread");
-    const int srow = (int)threadIdx.x < C::kRows ? (int)threadIdx.x : C::kRows - 1;
-    const uint8_t* const sp = (srow < BT ? SA : SW) + (int64_t)local(srow) * a.nb;
-    auto scales = [&](int i, uint8_t* buf) {
-        uint32_t lo = 0, hi = 0;
+    auto fill = [&] {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            lo |= (uint32_t)(8 * i + b < a.nb ? sp[8 * i + b] : 127) << (8 * b);
-            hi |= (uint32_t)(8 * i + 4 + b < a.nb ? sp[8 * i + 4 + b] : 127) << (8 * b);
+        for (int s = 0; s < ST; ++s)
+            if (s < nk) issue(s);
+    };
+    // Exponents of step i through registers: in the last step the blocks behind the
+    // last one count as 2^0 (their codes are zeros).
+    auto scales = [=, nb = a.nb](const uint8_t* sa, const uint8_t* sw, int rt, int rn, int i, uint8_t* buf) {
+        for (int r = threadIdx.x; r < C::kRows; r += C::kThreads) {
+            const uint8_t* p = (r < BT ? sa : sw) + (int64_t)local(r, rt, rn) * nb + 8 * i;
+            uint64_t w = 0;
+            if (8 * i + 8 <= nb) {
+                w = *(const u64_any*)p;
+            } else {
+#pragma unroll
+                for (int b = 0; b < 8; ++b) w |= (uint64_t)(8 * i + b < nb ? p[b] : 127) << (8 * b);
+            }
+            *(uint64_t*)(buf + C::kCodes + r * 8) = w;
         }
-        if ((int)threadIdx.x < C::kRows) *(u32x2*)(buf + C::kCodes + srow * 8) = u32x2{lo, hi};
     };
 
+    int at = blockIdx.x, turn = 0;
+    bool stored = false;  // S stores or more of the tile before are behind the first steps' loads
+    enter(at, bias[0]);
+    fill();
+    for (;;) {
+        f32x16 acc[C::NT][C::TT];
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s)
-        if (s < nk) issue(s);
-    for (int i = 0; i < nk; ++i) {
-        uint8_t* buf = ring + (i % ST) * C::kStage;
-        if constexpr (!WORDS) {
-            // the stage that this buffer held before is read by all waves: a barrier
-            // lies behind its MFMAs
-            scales(i, buf);
-            wait_vmcnt<0>();
-        } else {
-            // step i has landed: at most the loads of the ST - 2 later ones are out
-            if (ST > 2 && i + ST - 2 < nk) wait_vmcnt<(ST - 2) * (C::kPerWave + C::kScales)>();
+        for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+            for (int j = 0; j < C::TT; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        for (int i = 0; i < nk; ++i) {
+            uint8_t* buf = ring + (i % ST) * C::kStage;
+            if constexpr (!WORDS) scales(SA, SW, rows_t, rows_n, i, buf);  // all waves have read what it held
+            // Step i has landed if at most the loads behind its own are out: those of the ST - 1
+            // (at first) or ST - 2 later steps, and the stores. (The counter goes down in the
+            // order of issue, loads and stores alike.)
+            if (MANY && ST == 2 && WORDS && stored && i < 2) {
+                if (i == 0 && nk > 1) wait_vmcnt<L + S>();
+                else wait_vmcnt<S>();
+            } else if (WORDS && i == 0 && nk >= ST) wait_vmcnt<(ST - 1) * L>();
+            else if (WORDS && ST > 2 && i > 0 && i + ST - 2 < nk) wait_vmcnt<(ST - 2) * L>();
             else wait_vmcnt<0>();
+            block_barrier();  // all waves' loads of step i landed; step i - 1 is read
+            if (i > 0 && i + ST - 1 < nk) issue(i + ST - 1);
+            multiply<C>(buf, w_row, a_row, acc);
         }
-        block_barrier();  // all waves' loads of step i landed; step i - 1 is read
-        if (i + ST - 1 < nk) issue(i + ST - 1);
-        multiply<C>(buf, w_row, a_row, acc);
-    }
-    if (a.nb & 7) {
-        // the blocks behind the last whole step, zeros behind them; step nk - ST, which
-        // held this buffer, was read before the last barrier
-        uint8_t* buf = ring + (nk % ST) * C::kStage;
-        for (int c = threadIdx.x; c < C::kRows * 8; c += C::kThreads) {
-            const int r = c / 8, b = nk * 8 + c % 8;
-            const uint8_t* src = (r < BT ? A : W) + (int64_t)local(r) * row_bytes;
-            *(i32x4*)(buf + r * C::KB + place<C::KB>(r, c % 8) * 16) = b < a.nb ? *(const i32x4*)(src + b * 16) : i32x4{};
+        if (a.nb & 7) {
+            // the blocks behind the last whole step, zeros behind them; step nk - ST, which
+            // held this buffer, was read before the last barrier
+            uint8_t* buf = ring + (nk % ST) * C::kStage;
+            for (int c = threadIdx.x; c < C::kRows * 8; c += C::kThreads) {
+                const int r = c / 8, b = nk * 8 + c % 8;
+                const uint8_t* src = (r < BT ? A : W) + (int64_t)local(r, rows_t, rows_n) * row_bytes;
+                *(i32x4*)(buf + r * C::KB + place<C::KB>(r, c % 8) * 16) = b < a.nb ? *(const i32x4*)(src + b * 16) : i32x4{};
+            }
+            scales(SA, SW, rows_t, rows_n, nk, buf);
+            block_barrier();
+            multiply<C>(buf, w_row, a_row, acc);
         }
-        scales(nk, buf);
-        block_barrier();
-        multiply<C>(buf, w_row, a_row, acc);
+        __syncthreads();  // the ring is read, the bias written
+        const int64_t t_done = t0;
+        const int n_done = n0;
+        const float* bs = bias[turn];
+        const bool more = MANY && at + (int)gridDim.x < tiles;
+        const bool turned = (a.N & 3) != 0;  // outputs go through the ring
+        if (more) {
+            stored = !turned && rows_t == BT && rows_n == BN;
+            at += gridDim.x;
+            turn ^= 1;
+            enter(at, bias[turn]);
+            if (!turned) fill();
+        }
+        store_tile<C::NT, C::TT>(a, acc, bs, t_done, n_done, a_row, wn, wave, ring);
+        if (!more) break;
+        if (turned) {
+            __syncthreads();
+            fill();
+        }
     }
-    __syncthreads();  // bs is written, the ring is read
-    store_tile<C::NT, C::TT>(a, acc, bs, t0, n0, a_row, wn, wave, ring);
 }
 
 // TT x 16 tokens by 16 channels per workgroup; KW waves split k in steps of 4 blocks.
@@ -345,14 +381,16 @@ __global__ __launch_bounds__(KW * 64) void few_mx4_kernel(Mx4LinearArgs a)
 int64_t tiles(int64_t n, int b) { return (n + b - 1) / b; }
 bool words_ok(const Mx4LinearArgs& a) { return a.nb % 4 == 0 && (((uintptr_t)a.a_scale | (uintptr_t)a.w_scale) & 3) == 0; }
 
-template <int BT, int BN, int WT, int WN, int ST>
+// PER_CU: workgroups that a CU's LDS holds, each of which takes many tiles (0: one).
+template <int BT, int BN, int WT, int WN, int ST, int PER_CU>
 void run_tiles(Mx4LinearArgs a, hipStream_t stream)
 {
     a.tiles_t = (int32_t)tiles(a.T, BT);
     a.tiles_n = (int32_t)tiles(a.N, BN);
-    const dim3 grid((unsigned)(a.tiles_t * a.tiles_n)), block(WT * WN * 64);
-    if (words_ok(a)) hipLaunchKernelGGL((tile_mx4_kernel<BT, BN, WT, WN, ST, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((tile_mx4_kernel<BT, BN, WT, WN, 2, false>), grid, block, 0, stream, a);
+    const int64_t all = (int64_t)a.tiles_t * a.tiles_n, most = (int64_t)device_cu_count() * PER_CU;
+    const dim3 grid((unsigned)(PER_CU == 0 || all < most ? all : most)), block(WT * WN * 64);
+    if (words_ok(a)) hipLaunchKernelGGL((tile_mx4_kernel<BT, BN, WT, WN, ST, true, (PER_CU > 0)>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((tile_mx4_kernel<BT, BN, WT, WN, 2, false, false>), dim3((unsigned)all), block, 0, stream, a);
 }
 
 template <int TT>
@@ -368,9 +406,9 @@ void linear_once(const Mx4LinearArgs& a, hipStream_t stream)
     const int64_t cus = device_cu_count();
     if (a.T <= 16) run_few<1>(a, stream);
     else if (a.T <= 32) run_few<2>(a, stream);
-    else if (tiles(a.T, 256) * tiles(a.N, 256) >= cus) run_tiles<256, 256, 2, 4, 2>(a, stream);
-    else if (tiles(a.T, 128) * tiles(a.N, 128) >= 2 * cus) run_tiles<128, 128, 2, 2, 2>(a, stream);
-    else run_tiles<64, 64, 2, 2, 4>(a, stream);
+    else if (tiles(a.T, 256) * tiles(a.N, 256) >= cus && a.N > 128) run_tiles<256, 256, 2, 4, 2, 0>(a, stream);
+    else if (tiles(a.T, 128) * tiles(a.N, 128) >= cus) run_tiles<128, 128, 2, 2, 2, 2>(a, stream);
+    else run_tiles<64, 64, 2, 2, 4, 0>(a, stream);
 }
 
 }  // namespace
