@@ -32,7 +32,10 @@ hipError_t launch_fwd_mx4(Mx4FwdArgs a, hipStream_t stream)
     a.ntq = (int32_t)pieces(a.Lq, 32);
     const int64_t tiles = a.Nq * a.ntq;
     const int64_t most = tiles * a.Nd / ((int64_t)device_cu_count() * 8);
-    const int n = (int)(most < tiles ? (most > 1 ? most : 1) : tiles);
+    int n = (int)(most < tiles ? (most > 1 ? most : 1) : tiles);
+    // a query of a few tiles stays in one wave, a longer one in one pass of four
+    const int least = a.ntq <= 4 ? a.ntq : (a.ntq + 3) / 4;
+    n = n > least ? n : least;
     if (a.nb > 8) {
         launch_fwd_mx4_wide(a, n, stream);
     } else if (a.nb <= 4) {

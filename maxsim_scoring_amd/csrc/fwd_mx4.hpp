@@ -59,6 +59,14 @@ __device__ __forceinline__ uint32_t mask_word(const uint8_t* p, int n)
 
 __device__ __forceinline__ float vmax(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
+// Sum over the wave, the same in every lane.
+__device__ __forceinline__ float wave_sum(float v)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, row16_sum(v));
+    return (as_float(__builtin_amdgcn_readlane(b, 0)) + as_float(__builtin_amdgcn_readlane(b, 16))) +
+           (as_float(__builtin_amdgcn_readlane(b, 32)) + as_float(__builtin_amdgcn_readlane(b, 48)));
+}
+
 // The largest of 16 values and m, NaN where one is.
 __device__ __forceinline__ float max16(const f32x16& v, float m)
 {
@@ -193,31 +201,66 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                 __builtin_amdgcn_wave_barrier();
             }
 
-            // Sums of a finished document, tile by tile in order.
+            // Sums of a finished document, tiles in order. Both halves of a wave hold the
+            // maxima of 32 columns, over different rows: the halves of two tiles are swapped so
+            // that one maximum joins both, the first tile's in the low half.
             auto finish = [&](int doc) {
-                float sum = 0.0f;
                 int i = i0, at = 0;  // the query of tile n, and which of its tiles that is
-                static_for<0, NTW>([&](auto n) {
+                float sums = 0.0f;   // of this lane's columns of the query's tiles so far
+                auto put = [&](int n, int idx) {
+                    const int s = (SPLIT ? first + n : at) * 32 + col;
+                    if (s < Lq) a.argmax[(i * a.Nd + doc) * Lq + s] = idx;
+                };
+                static_for<0, (NTW + 1) / 2>([&](auto pair) {
+                    constexpr int n = 2 * pair, n2 = n + 1 < NTW ? n + 1 : n;
                     if (!SPLIT && i >= i0 + nq) return;
                     if (SPLIT && first + n >= ntq) return;
-                    float v = m[n];
-                    const float o = shfl_xor_f(v, 32);
-                    if constexpr (ARGMAX) {
-                        const int oi = shfl_xor_i(best[n], 32);
-                        const int idx = o > v || (o == v && oi < best[n]) ? oi : best[n];
-                        const int s = (SPLIT ? first + n : at) * 32 + col;
-                        if (h == 0 && s < Lq) a.argmax[(i * a.Nd + doc) * Lq + s] = idx;
+                    float v;
+                    if constexpr (n2 > n) {
+                        const auto both = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, m[n]),
+                                                                           __builtin_bit_cast(uint32_t, m[n2]), false, false);
+                        v = vmax(as_float(both[0]), as_float(both[1]));
+                    } else {
+                        v = vmax(m[n], shfl_xor_f(m[n], 32));
                     }
-                    v = any && ((live >> n) & 1) ? vmax(v, o) : 0.0f;
-                    sum += lanes0_31_sum(v);
-                    if (!SPLIT && ++at == ntq) {
-                        if (lane == 0) a.scores[i * a.Nd + doc] = sum;
-                        sum = 0.0f;
-                        at = 0;
-                        ++i;
+                    const bool mine = (live >> (n2 > n && h ? n2 : n)) & 1;
+                    v = any && mine && (n2 > n || h == 0) ? v : 0.0f;
+                    if constexpr (ARGMAX) {
+                        // the lower index of equal maxima
+                        static_for<n, n2 + 1>([&](auto k) {
+                            const float o = shfl_xor_f(m[k], 32);
+                            const int oi = shfl_xor_i(best[k], 32);
+                            best[k] = o > m[k] || (o == m[k] && oi < best[k]) ? oi : best[k];
+                        });
+                    }
+                    if constexpr (SPLIT) {
+                        if constexpr (ARGMAX) {
+                            if (h == 0) put(n, best[n]);
+                            if (n2 > n && h == 0) put(n2, best[n2]);
+                        }
+                        sums += v;  // (tiles behind the last one have no column that counts)
+                    } else {
+                        static_for<n, n2 + 1>([&](auto k) {
+                            if (i >= i0 + nq) return;
+                            if constexpr (ARGMAX) {
+                                if (h == 0) put(k, best[k]);
+                            }
+                            // the pair's low half is tile n, its high half tile n2
+                            sums += (k == n) == (h == 0) ? v : 0.0f;
+                            if (++at == ntq) {
+                                const float sum = wave_sum(sums);
+                                if (lane == 0) a.scores[i * a.Nd + doc] = sum;
+                                sums = 0.0f;
+                                at = 0;
+                                ++i;
+                            }
+                        });
                     }
                 });
-                if (SPLIT && lane == 0) part[wave][doc - b0] = sum;
+                if constexpr (SPLIT) {
+                    const float sum = wave_sum(sums);
+                    if (lane == 0) part[wave][doc - b0] = sum;
+                }
                 reset();
                 any = false;
             };
@@ -378,7 +421,7 @@ void run(Mx4FwdArgs a, hipStream_t stream)
         if (split) hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, true>), grid, block, 0, stream, a);      \
         else hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, false>), grid, block, 0, stream, a);           \
     } while (0)
-    if constexpr (NTW < 8 && NTW * G < 24) {
+    if constexpr (NTW < 4 || (NTW == 4 && G < 4)) {
         if (a.argmax && fast) MAXSIM_MX4_SPLIT(true, true);
         else if (a.argmax) MAXSIM_MX4_SPLIT(true, false);
     }

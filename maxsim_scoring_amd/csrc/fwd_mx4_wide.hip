@@ -11,7 +11,8 @@ void launch_fwd_mx4_wide(const Mx4FwdArgs& a, int n, hipStream_t stream)
         if (n >= 3) run<3, 4, 2, 8>(a, stream);
         else run<3, 1, 2, 12>(a, stream);
     } else if (a.nb <= 16) {
-        if (n >= 3) run<4, 4, 2, 8>(a, stream);
+        if (n >= 3 && !a.argmax) run<4, 4, 2, 8>(a, stream);
+        else if (n >= 2) run<4, 2, 2, 8>(a, stream);
         else run<4, 1, 2, 8>(a, stream);
     } else if (a.nb <= 24) {
         if (n >= 3 && !a.argmax) run<6, 4, 2, 4>(a, stream);
@@ -19,7 +20,7 @@ void launch_fwd_mx4_wide(const Mx4FwdArgs& a, int n, hipStream_t stream)
         else run<6, 1, 2, 8>(a, stream);
     } else {
         if (n >= 2) run<8, 2, 2, 4>(a, stream);
-        else run<8, 1, 1, 8>(a, stream);
+        else run<8, 1, 2, 4>(a, stream);
     }
 }
 

@@ -410,6 +410,15 @@ __device__ __forceinline__ int target_of(const LogprobArgs& a, int64_t i, int p,
     return c;
 }
 
+// The largest float below x (-Inf below the lowest); NaN for NaN.
+__device__ __forceinline__ float float_below(float x)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    if (x != x) return x;
+    if (x == 0.0f) return -0x1p-149f;
+    return as_float(x > 0.0f ? b - 1 : b + 1);
+}
+
 // 2^t of scores against the largest, t at least -200 (where 2^t is 0): so for -Inf,
 // and in rows without candidates.
 __device__ __forceinline__ float t_of(float x, float m, float c) { return __builtin_fmaxf((x - m) * c, -200.0f); }
@@ -479,16 +488,21 @@ __global__ __launch_bounds__(T) void logprob_part_kernel(LogprobArgs a)
             const float xt = lane_of(tx, p);
             const int t = lane_of(tc, p) - c0;  // relative to the chunk
             if (xt == -__builtin_inff()) continue;
-            // equal scores come before the target if their column does: none of a
-            // chunk behind it, all of one in front of it
+            // Equal scores come before the target if their column does: none of a chunk
+            // behind it, all of one in front of it. x >= xt is x > the float below xt. (The
+            // counts stay in vector registers: a ballot and a bit count for each register
+            // wait for each other.)
+            const float below = float_below(xt);
             uint32_t n = 0;
-            auto count = [&](auto before) {
+            if (t < 0 || t >= Y::kColumns) {
+                const float least = t < 0 ? xt : below;
 #pragma unroll
-                for (int v = 0; v < N; ++v) n += (uint32_t)__builtin_popcountll(__ballot(before(v)));
-            };
-            if (t < 0) count([&](int v) { return x[v] > xt; });
-            else if (t >= Y::kColumns) count([&](int v) { return x[v] >= xt; });
-            else count([&](int v) { return x[v] > xt || (x[v] == xt && Y::place(v) < t); });
+                for (int v = 0; v < N; ++v) n += x[v] > least;
+            } else {
+#pragma unroll
+                for (int v = 0; v < N; ++v) n += x[v] > (Y::place(v) < t ? below : xt);
+            }
+            n = wave_reduce(n, AddOp{});
             mine = lane == p ? n : mine;
         }
         counts[wave][lane] = mine;
@@ -724,15 +738,17 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
     }
 }
 
-// Rows of up to 1024 columns take one wave, with as few columns a thread as one load
-// brings where that is enough.
+// One wave takes a row of as many columns as one load a lane brings, four waves one of
+// four times as many: where they would have 16 columns a lane, the targets' ranks and
+// the ordering of the best keep a wave busy (16 rows of 752 columns with 32 targets
+// 32 us).
 template <int E>
 void forward(const LogprobArgs& a, hipStream_t stream)
 {
     constexpr int V = Layout<E, 64, kLpValues>::V;
     const dim3 rows((unsigned)a.Nq), chunks((unsigned)(a.Nq * a.chunks));
     if (a.Nd <= 64 * V) hipLaunchKernelGGL((logprob_part_kernel<E, 64, V, true>), rows, dim3(64), 0, stream, a);
-    else if (a.Nd <= 64 * kLpValues) hipLaunchKernelGGL((logprob_part_kernel<E, 64, kLpValues, true>), rows, dim3(64), 0, stream, a);
+    else if (a.Nd <= 256 * V) hipLaunchKernelGGL((logprob_part_kernel<E, 256, V, true>), rows, dim3(256), 0, stream, a);
     else if (a.chunks == 1) hipLaunchKernelGGL((logprob_part_kernel<E, 256, kLpValues, true>), rows, dim3(256), 0, stream, a);
     else {
         hipLaunchKernelGGL((logprob_part_kernel<E, 256, kLpValues, false>), chunks, dim3(256), 0, stream, a);

@@ -405,7 +405,7 @@ void linear_once(const Mx4LinearArgs& a, hipStream_t stream)
 {
     const int64_t cus = device_cu_count();
     if (a.T <= 16) run_few<1>(a, stream);
-    else if (a.T <= 32) run_few<2>(a, stream);
+    else if (a.T <= 32 || tiles(a.T, 32) * tiles(a.N, 16) <= cus) run_few<2>(a, stream);
     else if (tiles(a.T, 256) * tiles(a.N, 256) >= cus && a.N > 128) run_tiles<256, 256, 2, 4, 2, 0>(a, stream);
     else if (tiles(a.T, 128) * tiles(a.N, 128) >= cus) run_tiles<128, 128, 2, 2, 2, 2>(a, stream);
     else run_tiles<64, 64, 2, 2, 4, 0>(a, stream);

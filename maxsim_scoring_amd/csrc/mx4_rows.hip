@@ -414,6 +414,7 @@ void quantize(const Mx4RowArgs& a, bool normalize, hipStream_t stream)
     else if (units <= 128) MAXSIM_MX4_NORM(64, 2);
     else if (units <= 256) MAXSIM_MX4_NORM(64, 4);
     else if (units <= 512) MAXSIM_MX4_NORM(64, 8);
+    else if (units <= 1024) MAXSIM_MX4_NORM(64, 16);
     else hipLaunchKernelGGL((quantize_mx4_norm_long_kernel<E, WHOLE>), grid, block, 0, stream, a);
 #undef MAXSIM_MX4_NORM
 }
