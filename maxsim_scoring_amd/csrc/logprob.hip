@@ -481,30 +481,51 @@ __global__ __launch_bounds__(T) void logprob_part_kernel(LogprobArgs a)
     put(red_t, sum_t);
 
     // ---- how many come before each target, 64 targets at a time --------------
+    // Equal scores come before the target if their column does: none of a chunk behind
+    // it, all of one in front of it. x >= xt is x > the float below xt. Four targets at
+    // a time, two in the halves of a word when they are added up over the wave. (A
+    // ballot and a bit count for each register instead wait for each other.)
     auto count_before = [&](int p0) {  // that of target p0 + lane
         const int np = a.P - p0 < 64 ? a.P - p0 : 64;
         uint32_t mine = 0;
-        for (int p = 0; p < np; ++p) {
-            const float xt = lane_of(tx, p);
-            const int t = lane_of(tc, p) - c0;  // relative to the chunk
-            if (xt == -__builtin_inff()) continue;
-            // Equal scores come before the target if their column does: none of a chunk
-            // behind it, all of one in front of it. x >= xt is x > the float below xt. (The
-            // counts stay in vector registers: a ballot and a bit count for each register
-            // wait for each other.)
-            const float below = float_below(xt);
-            uint32_t n = 0;
-            if (t < 0 || t >= Y::kColumns) {
-                const float least = t < 0 ? xt : below;
+        auto some = [&](auto width, int p) {
+            constexpr int M = width;
+            float xt[M], least[M];
+            int t[M];
+            bool here = false;
 #pragma unroll
-                for (int v = 0; v < N; ++v) n += x[v] > least;
+            for (int k = 0; k < M; ++k) {
+                xt[k] = lane_of(tx, p + k);
+                t[k] = lane_of(tc, p + k) - c0;
+                here |= t[k] >= 0 && t[k] < Y::kColumns;
+                least[k] = t[k] < 0 ? xt[k] : float_below(xt[k]);
+            }
+            uint32_t n[M] = {};
+            if (here) {
+#pragma unroll
+                for (int v = 0; v < N; ++v)
+#pragma unroll
+                    for (int k = 0; k < M; ++k) n[k] += x[v] > (Y::place(v) < t[k] ? least[k] : xt[k]);
             } else {
 #pragma unroll
-                for (int v = 0; v < N; ++v) n += x[v] > (Y::place(v) < t ? below : xt);
+                for (int v = 0; v < N; ++v)
+#pragma unroll
+                    for (int k = 0; k < M; ++k) n[k] += x[v] > least[k];
             }
-            n = wave_reduce(n, AddOp{});
-            mine = lane == p ? n : mine;
-        }
+            if constexpr (M == 1) {
+                const uint32_t all = wave_reduce(n[0], AddOp{});
+                mine = lane == p ? all : mine;
+            } else {
+#pragma unroll
+                for (int k = 0; k < M; k += 2) {
+                    const uint32_t both = wave_reduce(n[k] | n[k + 1] << 16, AddOp{});
+                    mine = lane == p + k ? both & 0xffffu : lane == p + k + 1 ? both >> 16 : mine;
+                }
+            }
+        };
+        int p = 0;
+        for (; p + 4 <= np; p += 4) some(std::integral_constant<int, 4>{}, p);
+        for (; p < np; ++p) some(std::integral_constant<int, 1>{}, p);
         counts[wave][lane] = mine;
     };
     auto counted = [&] {
@@ -567,8 +588,24 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
     const int total = a.K ? a.chunks * a.cap : 0;  // candidates, 0 where a chunk had fewer
     const bool in_registers = total <= T * kJoinHeld;
     const uint64_t* from = a.ws_cand + u0 * a.cap;
-    float tx;
-    int tc = target_of<E>(a, i, threadIdx.x, tx);
+    // What the row's outputs need is loaded at once: every dependent load would add
+    // a memory latency to the few workgroups' time.
+    const int tid = threadIdx.x;
+    float tx, first_top = -__builtin_inff();
+    double first_sum = 0.0, first_t = 0.0;
+    int tc = target_of<E>(a, i, tid, tx);
+    if (tid < a.chunks) {
+        first_top = a.ws_top[u0 + tid];
+        first_sum = a.ws_sums[2 * (u0 + tid)];
+        first_t = a.ws_sums[2 * (u0 + tid) + 1];
+    }
+    auto count_of = [&](int p) {
+        uint32_t n = 0;
+#pragma unroll 8
+        for (int c = 0; c < a.chunks; ++c) n += a.ws_rank[(u0 + c) * a.P + p];
+        return n;
+    };
+    uint32_t before = a.rank && tid < a.P ? count_of(tid) : 0;
     uint64_t o[kJoinHeld];
     uint32_t least = 0xffffffffu, have = 0;
     for (int e0 = 0; e0 < total; e0 += kJoinHeld * T) {
@@ -583,8 +620,8 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
             least = o[k] != 0 ? MinOp{}(least, (uint32_t)(o[k] >> a.cbits)) : least;
         }
     }
-    float m = -__builtin_inff();
-    for (int c = threadIdx.x; c < a.chunks; c += T) m = MaxOp{}(m, a.ws_top[u0 + c]);
+    float m = first_top;
+    for (int c = tid + T; c < a.chunks; c += T) m = MaxOp{}(m, a.ws_top[u0 + c]);
     m = wave_reduce(m, MaxOp{});
     put(red_m, m);
     least = wave_reduce(least, MinOp{});
@@ -596,12 +633,14 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
 
     const float scale2 = a.scale * 0x1.715476p0f;
     double sum = 0.0, sum_t = 0.0;
-    for (int c = threadIdx.x; c < a.chunks; c += T) {
-        const float t = t_of(a.ws_top[u0 + c], m, scale2);
-        const double e = (double)__builtin_amdgcn_exp2f(t), s = a.ws_sums[2 * (u0 + c)];
+    auto add = [&](float top, double s, double st) {
+        const float t = t_of(top, m, scale2);
+        const double e = (double)__builtin_amdgcn_exp2f(t);
         sum = __builtin_fma(e, s, sum);
-        sum_t = __builtin_fma(e, __builtin_fma((double)t, s, a.ws_sums[2 * (u0 + c) + 1]), sum_t);
-    }
+        sum_t = __builtin_fma(e, __builtin_fma((double)t, s, st), sum_t);
+    };
+    if (tid < a.chunks) add(first_top, first_sum, first_t);
+    for (int c = tid + T; c < a.chunks; c += T) add(a.ws_top[u0 + c], a.ws_sums[2 * (u0 + c)], a.ws_sums[2 * (u0 + c) + 1]);
     sum = wave_reduce(sum, AddOp{});
     sum_t = wave_reduce(sum_t, AddOp{});
     put(red_sum, sum);
@@ -611,14 +650,12 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
     sum_t = joined(red_t, sum_t, AddOp{});
     const double L = log(sum);
     if (threadIdx.x == 0) write_stats(a, i, m, sum, sum_t, L);
-    for (int p = threadIdx.x; p < a.P; p += T) {
-        if (p >= T) tc = target_of<E>(a, i, p, tx);
-        uint32_t n = 0;
-        if (a.rank) {
-#pragma unroll 8
-            for (int c = 0; c < a.chunks; ++c) n += a.ws_rank[(u0 + c) * a.P + p];
+    for (int p = tid; p < a.P; p += T) {
+        if (p >= T) {
+            tc = target_of<E>(a, i, p, tx);
+            before = a.rank ? count_of(p) : 0;
         }
-        write_target(a, i, p, tc, tx, n, m, L);
+        write_target(a, i, p, tc, tx, before, m, L);
     }
     if (a.K == 0) return;
 
