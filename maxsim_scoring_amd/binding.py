@@ -1021,7 +1021,7 @@ def maxsim_logprob_fwd(X: torch.Tensor, targets: torch.Tensor, mask: Optional[to
     _has("entropy", entropy, torch.float32, (Nq,))
     _has("top_idx", top_idx, torch.int32, (Nq, k))
     _has("top_logp", top_logp, torch.float32, (Nq, k))
-    need = lib().maxsim_logprob_workspace(Nq, Nd, P, k)
+    need = lib().maxsim_logprob_workspace(Nq, Nd, P, k) if Nd > 4096 else 0
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.numel() < need):
         raise ValueError(f"workspace must be uint8 of at least {need} bytes")
     index = _place("X targets mask logp rank norm entropy top_idx top_logp workspace", X, targets, mask,

@@ -83,33 +83,50 @@ __device__ __forceinline__ void load_columns(const LogprobArgs& a, int64_t i, in
 #pragma unroll
     for (int g = 0; g < N / Y::V; ++g) {
         const int at = Y::place(g * Y::V);
-        u32x4 w = {0, 0, 0, 0};
-        uint32_t keep[Y::V / 4];
-#pragma unroll
-        for (int k = 0; k < Y::V / 4; ++k) keep[k] = 0;
+        u32x4 w;
         if (at + Y::V <= n) {
             w = *(const u32x4_any*)(p + (int64_t)at * elem_bytes<E>());
-#pragma unroll
-            for (int k = 0; k < Y::V / 4; ++k) keep[k] = mp ? *(const u32_any*)(mp + at + 4 * k) : 0x01010101u;
         } else {
+            // -Inf behind the end: 0xff800000, 0xff80 or 0xfc00
+            constexpr uint32_t kNone = E == kF32 ? 0xff800000u : E == kBF16 ? 0xff80ff80u : 0xfc00fc00u;
+            w = u32x4{kNone, kNone, kNone, kNone};
 #pragma unroll
             for (int e = 0; e < Y::V; ++e) {
                 if (at + e >= n) continue;
                 if constexpr (E == kF32) w[e] = ((const uint32_t*)p)[at + e];
-                else w[e / 2] |= (uint32_t)((const uint16_t*)p)[at + e] << (16 * (e & 1));
-                keep[e / 4] |= (mp ? (uint32_t)mp[at + e] : 1u) << (8 * (e & 3));
+                else {
+                    const uint32_t b = ((const uint16_t*)p)[at + e];
+                    w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | b << 16 : (w[e / 2] & 0xffff0000u) | b;
+                }
             }
         }
 #pragma unroll
         for (int e = 0; e < Y::V; ++e) {
-            float v;
-            if constexpr (E == kF32) v = as_float(w[e]);
+            if constexpr (E == kF32) x[g * Y::V + e] = as_float(w[e]);
             else {
                 const uint32_t bits = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-                v = E == kBF16 ? __builtin_bit_cast(float, bits << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+                x[g * Y::V + e] = E == kBF16 ? as_float(bits << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
             }
-            x[g * Y::V + e] = (keep[e / 4] >> (8 * (e & 3))) & 0xffu ? v : -__builtin_inff();
         }
+    }
+    if (!mp) return;
+#pragma unroll
+    for (int g = 0; g < N / Y::V; ++g) {
+        const int at = Y::place(g * Y::V);
+        uint32_t keep[Y::V / 4];
+#pragma unroll
+        for (int k = 0; k < Y::V / 4; ++k) {
+            keep[k] = 0;
+            if (at + Y::V <= n) keep[k] = *(const u32_any*)(mp + at + 4 * k);
+            else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (at + 4 * k + e < n) keep[k] |= (uint32_t)mp[at + 4 * k + e] << (8 * e);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < Y::V; ++e)
+            x[g * Y::V + e] = (keep[e / 4] >> (8 * (e & 3))) & 0xffu ? x[g * Y::V + e] : -__builtin_inff();
     }
 }
 
@@ -306,54 +323,77 @@ struct Far {
 };
 
 // Picks the best columns into to[0, n), n <= cap, in any order. least, top: the range
-// of the candidates' keys; have: how many there are in all. counter: 0.
+// of the candidates' keys; have: how many there are in all; threads: how many of the
+// workgroup's hold one; best: this thread's largest key (0: it holds none). counter: 0.
+//
+// A bound that K threads' largest keys reach has K candidates at or above it, and for
+// K up to half of the threads seldom many more; it takes one number of each thread.
+// Only where they are too many are all candidates looked at.
 template <int T, typename Source>
-__device__ __forceinline__ uint32_t pick(const Source& from, int have, uint32_t least, uint32_t top, const LogprobArgs& a,
-                                         uint64_t* to, uint32_t* hist, uint32_t* counter)
+__device__ __forceinline__ uint32_t pick(const Source& from, int have, int threads, uint32_t best, uint32_t least, uint32_t top,
+                                         const LogprobArgs& a, uint64_t* to, uint32_t* hist, uint32_t* counter)
 {
     const uint32_t K = (uint32_t)a.K, cap = (uint32_t)a.cap;
-    uint32_t key = least, above = 0, upto = (uint32_t)have;
-    uint64_t border = 0;  // of the numbers that are taken, where equal keys are told apart
-    if (upto > cap) {
-        key = select_bound<T, uint32_t>(
-            [&](auto f) {
-                from.for_all([&](int v) {
-                    if (from.is(v)) f(from.key(v));
-                });
-            },
-            K, cap, least, top, above, upto, hist);
-        if (upto > cap)
-            border = select_bound<T, uint64_t>(
-                [&](auto f) {
-                    from.for_all([&](int v) {
-                        if (from.is(v) && from.key(v) == key) f(from.number(v));
-                    });
-                },
-                K, cap, order_of(key, a.Nd - 1, a.cbits), order_of(key, 0, a.cbits), above, upto, hist);
-    }
-    const Bound b = {key, score_of(key), (uint64_t)key << a.cbits};
     // a wave takes a run of places; which one depends on the waves' timing, the
     // outputs do not: they are ordered later
     auto copy = [&](auto taken) {
         uint32_t mine = 0;
         from.for_all([&](int v) { mine += (uint32_t)__builtin_popcountll(__ballot(taken(v))); });
-        if (mine == 0) return;
-        uint32_t at = 0;
-        if (lane_id() == 0) at = atomicAdd(counter, mine);
-        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
-        from.for_all([&](int v) {
-            const bool t = taken(v);
-            const uint64_t all = __ballot(t);
-            if (all == 0) return;
-            const uint32_t place = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
-            if (t && place < cap) to[place] = from.number(v);
-            at += (uint32_t)__builtin_popcountll(all);
-        });
+        if (mine != 0) {
+            uint32_t at = 0;
+            if (lane_id() == 0) at = atomicAdd(counter, mine);
+            at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+            from.for_all([&](int v) {
+                const bool t = taken(v);
+                const uint64_t all = __ballot(t);
+                if (all == 0) return;
+                const uint32_t place = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+                if (t && place < cap) to[place] = from.number(v);
+                at += (uint32_t)__builtin_popcountll(all);
+            });
+        }
+        __syncthreads();
+        return *counter;
     };
-    if (border == 0) copy([&](int v) { return from.above(v, b); });
-    else copy([&](int v) { return from.is(v) && from.number(v) >= border; });
-    __syncthreads();
-    return *counter < cap ? *counter : cap;
+    auto copy_from = [&](uint32_t key) {
+        const Bound b = {key, score_of(key), (uint64_t)key << a.cbits};
+        return copy([&](int v) { return from.above(v, b); });
+    };
+    uint32_t key = least, above = 0, upto = (uint32_t)have;
+    if (upto > cap && 2 * K <= (uint32_t)T && K <= (uint32_t)threads) {
+        // (as many may be above it as there are threads: one round of bins is enough)
+        key = select_bound<T, uint32_t>(
+            [&](auto f) {
+                if (best != 0) f(best);
+            },
+            K, (uint32_t)T, least, top, above, upto, hist);
+        const uint32_t n = copy_from(key);
+        if (n <= cap) return n;
+        least = key;
+        above = 0;
+        upto = n;
+        __syncthreads();  // the counter is read
+        if (threadIdx.x == 0) *counter = 0;
+    }
+    if (upto <= cap) return copy_from(key);
+    key = select_bound<T, uint32_t>(
+        [&](auto f) {
+            from.for_all([&](int v) {
+                if (from.is(v)) f(from.key(v));
+            });
+        },
+        K, cap, least, top, above, upto, hist);
+    if (upto <= cap) return copy_from(key);
+    // equal keys are told apart by their columns
+    const uint64_t border = select_bound<T, uint64_t>(
+        [&](auto f) {
+            from.for_all([&](int v) {
+                if (from.is(v) && from.key(v) == key) f(from.number(v));
+            });
+        },
+        K, cap, order_of(key, a.Nd - 1, a.cbits), order_of(key, 0, a.cbits), above, upto, hist);
+    const uint32_t n = copy([&](int v) { return from.is(v) && from.number(v) >= border; });
+    return n < cap ? n : cap;
 }
 
 // Writes the K best of n <= kMaxCap numbers of cand (LDS) in order.
@@ -432,7 +472,7 @@ __global__ __launch_bounds__(T) void logprob_part_kernel(LogprobArgs a)
     __shared__ uint32_t hist[kBins + 4];
     __shared__ uint64_t cand[kMaxCap];
     __shared__ float red_m[W];
-    __shared__ uint32_t red_least[W], red_have[W], counter;
+    __shared__ uint32_t red_least[W], red_have[W], red_threads[W], counter;
     __shared__ double red_sum[W], red_t[W];
     __shared__ uint32_t counts[W][64];
 
@@ -446,9 +486,10 @@ __global__ __launch_bounds__(T) void logprob_part_kernel(LogprobArgs a)
     int tc = target_of<E>(a, i, lane, tx);
 
     float m = x[0];
-    uint32_t least = 0xffffffffu, have = 0;
+    uint32_t least = 0xffffffffu, have = 0, threads = 0, best = 0;
 #pragma unroll
     for (int v = 1; v < N; ++v) m = MaxOp{}(m, x[v]);
+    if (m > -__builtin_inff()) best = key_of(m);
     m = wave_reduce(m, MaxOp{});
     put(red_m, m);
     if (a.K) {
@@ -461,8 +502,10 @@ __global__ __launch_bounds__(T) void logprob_part_kernel(LogprobArgs a)
         }
         least = key_of(low);
         least = wave_reduce(least, MinOp{});
+        threads = (uint32_t)__builtin_popcountll(__ballot(best != 0));
         put(red_least, least);
         put(red_have, have);
+        put(red_threads, threads);
     }
     if (W > 1) __syncthreads();
     m = joined(red_m, m, MaxOp{});
@@ -563,7 +606,8 @@ __global__ __launch_bounds__(T) void logprob_part_kernel(LogprobArgs a)
     // ---- candidates for the best columns --------------------------------------
     have = joined(red_have, have, AddOp{});
     least = joined(red_least, least, MinOp{});
-    const uint32_t n = pick<T>(Scores<E, T, N>{x, c0, a.cbits}, (int)have, least, key_of(m), a, cand, hist, &counter);
+    threads = joined(red_threads, threads, AddOp{});
+    const uint32_t n = pick<T>(Scores<E, T, N>{x, c0, a.cbits}, (int)have, (int)threads, best, least, key_of(m), a, cand, hist, &counter);
     if constexpr (WHOLE) {
         write_best<T>(a, i, cand, (int)n, m, L);
     } else {
@@ -580,7 +624,7 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
     __shared__ uint32_t hist[kBins + 4];
     __shared__ uint64_t cand[kMaxCap];
     __shared__ float red_m[W];
-    __shared__ uint32_t red_least[W], red_have[W], counter;
+    __shared__ uint32_t red_least[W], red_have[W], red_threads[W], counter;
     __shared__ double red_sum[W], red_t[W];
 
     if (threadIdx.x == 0) counter = 0;
@@ -607,7 +651,7 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
     };
     uint32_t before = a.rank && tid < a.P ? count_of(tid) : 0;
     uint64_t o[kJoinHeld];
-    uint32_t least = 0xffffffffu, have = 0;
+    uint32_t least = 0xffffffffu, have = 0, best = 0;
     for (int e0 = 0; e0 < total; e0 += kJoinHeld * T) {
 #pragma unroll
         for (int k = 0; k < kJoinHeld; ++k) {
@@ -616,8 +660,10 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
         }
 #pragma unroll
         for (int k = 0; k < kJoinHeld; ++k) {
+            const uint32_t key = (uint32_t)(o[k] >> a.cbits);  // 0 of none
             have += o[k] != 0;
-            least = o[k] != 0 ? MinOp{}(least, (uint32_t)(o[k] >> a.cbits)) : least;
+            least = o[k] != 0 ? MinOp{}(least, key) : least;
+            best = key > best ? key : best;
         }
     }
     float m = first_top;
@@ -628,6 +674,8 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
     put(red_least, least);
     have = wave_reduce(have, AddOp{});
     put(red_have, have);
+    uint32_t threads = (uint32_t)__builtin_popcountll(__ballot(best != 0));
+    put(red_threads, threads);
     __syncthreads();
     m = joined(red_m, m, MaxOp{});
 
@@ -661,9 +709,10 @@ __global__ __launch_bounds__(kJoinThreads) void logprob_join_kernel(LogprobArgs 
 
     have = joined(red_have, have, AddOp{});
     least = joined(red_least, least, MinOp{});
+    threads = joined(red_threads, threads, AddOp{});
     const uint32_t n = in_registers
-        ? pick<T>(Numbers<kJoinHeld>{o, a.cbits}, (int)have, least, key_of(m), a, cand, hist, &counter)
-        : pick<T>(Far{from, total, T, a.cbits}, (int)have, least, key_of(m), a, cand, hist, &counter);
+        ? pick<T>(Numbers<kJoinHeld>{o, a.cbits}, (int)have, (int)threads, best, least, key_of(m), a, cand, hist, &counter)
+        : pick<T>(Far{from, total, T, a.cbits}, (int)have, (int)threads, best, least, key_of(m), a, cand, hist, &counter);
     write_best<T>(a, i, cand, (int)n, m, L);
 }
 
