@@ -14,8 +14,8 @@
  * rows, asynchronous on `stream`, no allocation, all checks on the host before
  * anything is enqueued, outputs alias neither inputs nor each other, results
  * bitwise reproducible run to run), with these additions:
- *   - Row i of X [Nq, Nd] holds scores; scale > 0 multiplies them (the inverse
- *     temperature). mask [Nq, Nd] uint8 0/1 or NULL: columns with mask 0 are not
+ *   - Row i of X [Nq, Nd] holds scores; scale, from 2^-64 to 2^64, multiplies
+ *     them (the inverse temperature). mask [Nq, Nd] uint8 0/1 or NULL: columns with mask 0 are not
  *     looked at. A column is a candidate if its mask is not 0 and its score is
  *     not -Inf. Scores of the type's lowest value are candidates like others.
  *   - targets [Nq, P] int32: columns; a column may be named more than once. An
@@ -57,8 +57,8 @@ int64_t maxsim_logprob_workspace(int64_t Nq, int64_t Nd, int64_t P, int64_t K);
  *        order of the ranks; -1 and -Inf where there are fewer. Not used with K = 0.
  *   X [Nq, Nd] of `dtype` (F16, BF16, F32)
  * Nq == 0 enqueues nothing. Errors: SHAPE (negative sizes, a workspace that is too
- * small), UNSUPPORTED (dtype, K > 1024, scale not positive and finite,
- * alignment), NULL, OVERFLOW (Nq, Nd or P >= 2^31 - 4096, Nq * ceil(Nd / 4096) or
+ * small), UNSUPPORTED (dtype, K > 1024, a scale outside its range, alignment),
+ * NULL, OVERFLOW (Nq, Nd or P >= 2^31 - 4096, Nq * ceil(Nd / 4096) or
  * Nq * P >= 2^31).
  */
 maxsim_status_t maxsim_logprob_fwd(maxsim_dtype_t dtype, const void* X, int64_t Nq, int64_t Nd,

@@ -396,6 +396,12 @@ __device__ __forceinline__ uint32_t pick(const Source& from, int have, int threa
     return n < cap ? n : cap;
 }
 
+// In float64, where neither the difference of two scores nor its product overflows.
+__device__ __forceinline__ float logp_of(const LogprobArgs& a, float x, float m, double L)
+{
+    return (float)((double)a.scale * ((double)x - (double)m) - L);
+}
+
 // Writes the K best of n <= kMaxCap numbers of cand (LDS) in order.
 template <int T>
 __device__ __forceinline__ void write_best(const LogprobArgs& a, int64_t i, const uint64_t* cand, int n, float m, double L)
@@ -408,7 +414,7 @@ __device__ __forceinline__ void write_best(const LogprobArgs& a, int64_t i, cons
         if (place < a.K) {
             const float x = score_of((uint32_t)(mine >> a.cbits));
             a.top_idx[i * a.K + place] = column_of(mine, a.cbits);
-            a.top_logp[i * a.K + place] = (float)((double)(a.scale * (x - m)) - L);
+            a.top_logp[i * a.K + place] = logp_of(a, x, m, L);
         }
     }
     for (int e = n + threadIdx.x; e < a.K; e += T) {
@@ -436,7 +442,7 @@ __device__ __forceinline__ void write_target(const LogprobArgs& a, int64_t i, in
 {
     const bool in = x != -__builtin_inff();
     float lp = c >= 0 ? x : 0.0f;
-    if (in || L != L) lp = (float)((double)(a.scale * (x - m)) - L);
+    if (in || L != L) lp = logp_of(a, x, m, L);
     a.logp[i * a.P + p] = lp;
     if (a.rank) a.rank[i * a.P + p] = in ? (int)before : -1;
 }

@@ -3,7 +3,6 @@
 #include "maxsim_loss.h"
 
 #include <climits>
-#include <cmath>
 
 #include "logprob.hpp"
 
@@ -20,7 +19,8 @@ bool float_ok(maxsim_dtype_t t) { return t == MAXSIM_F16 || t == MAXSIM_BF16 || 
 int elem_of(maxsim_dtype_t t) { return t == MAXSIM_F16 ? kF16 : t == MAXSIM_BF16 ? kBF16 : kF32; }
 uintptr_t bytes_of(maxsim_dtype_t t) { return t == MAXSIM_F32 ? 4 : 2; }
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-bool scale_ok(float s) { return s > 0.0f && s < INFINITY; }  // NaN is neither
+// Where a difference of scores overflows, its probability is 0; NaN is not in it.
+bool scale_ok(float s) { return s >= 0x1p-64f && s <= 0x1p64f; }
 
 int64_t chunks_of(int64_t Nd) { return Nd > kLpChunk ? (Nd + kLpChunk - 1) / kLpChunk : 1; }
 

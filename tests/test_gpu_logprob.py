@@ -258,6 +258,47 @@ def test_rows_beyond_32_bit_offsets(ms):
     _close("dX", dX[-2:], want, bound + np.abs(want) * HALF[torch.float16] + FLOOR[torch.float16])
 
 
+def test_many_rows(ms):
+    """More rows than one launch takes."""
+    Nq = (1 << 22) + 3
+    x = torch.zeros(Nq, 3, device=DEV)
+    x[-2:] = torch.tensor([[1.0, 5.0, 2.0], [7.0, -3.0, 7.5]], device=DEV)
+    t = torch.ones(Nq, 1, dtype=torch.int32, device=DEV)
+    out = ms.maxsim_logprob_fwd(x, t, k=2)
+    g = torch.ones(Nq, 1, device=DEV)
+    dX = ms.maxsim_logprob_bwd(x, t, out[2], g)
+    assert all(torch.equal(o[:1].expand_as(o[:-2]), o[:-2]) for o in (*out, dX))
+    want, bound = ref.forward(_np(x[-3:]), t[-3:].cpu().numpy(), None, 1.0, 2)
+    for name, o in zip(("logp", "rank", "norm", "entropy", "top_idx", "top_logp"), out):
+        if o.dtype == torch.int32:
+            assert np.array_equal(o[-3:].cpu().numpy(), want[name])
+        else:
+            _close(name, o[-3:], want[name], bound[name])
+    want, bound = ref.backward(_np(x[-3:]), t[-3:].cpu().numpy(), None, 1.0, _np(g[-3:]), _np(out[2][-3:]))
+    _close("dX", dX[-3:], want, bound)
+
+
+@pytest.mark.parametrize("Nd", [40, 6000])
+def test_the_whole_range_of_scores(ms, Nd):
+    """Differences of scores beyond the largest float: those columns' log probabilities
+    are finite after the scale, their probabilities 0."""
+    low, high, scale = -3.4028234663852886e38, 3.0e38, 2.0 ** -64
+    x = torch.full((1, Nd), low, device=DEV)
+    x[0, 5] = high
+    t = torch.tensor([[5, 0, Nd - 1]], dtype=torch.int32, device=DEV)
+    logp, rank, norm, entropy, top_idx, top_logp = ms.maxsim_logprob_fwd(x, t, scale=scale, k=3)
+    far = torch.tensor(scale * (low - float(x[0, 5])), dtype=torch.float64).float().item()
+    assert logp.tolist() == [[0.0, far, far]] and rank.tolist() == [[0, 1, Nd - 1]]
+    assert entropy.tolist() == [0.0] and top_idx.tolist() == [[5, 0, 1]] and top_logp.tolist() == [[0.0, far, far]]
+    dX = ms.maxsim_logprob_bwd(x, t, norm, torch.ones(1, 3, device=DEV), scale=scale, entropy=entropy,
+                               grad_entropy=torch.ones(1, device=DEV))
+    # the named ones 1, the sure one 1 - 3
+    want = torch.zeros(Nd, device=DEV)
+    want[0] = want[Nd - 1] = scale
+    want[5] = -2 * scale
+    assert torch.equal(dX[0], want)
+
+
 def test_unaligned_rows(ms):
     """Scores and masks at any element, as views into larger buffers."""
     for dtype in TYPES:

@@ -118,7 +118,7 @@ def test_logprob_refusals(L):
         for k in ("Nq", "Nd", "P"):
             assert f(**{k: -1}) == ERR_SHAPE, k
         assert f(dt=I8) == ERR_UNSUPPORTED
-        for s in (0.0, -1.0, float("nan"), float("inf")):
+        for s in (0.0, -1.0, float("nan"), float("inf"), 2.0 ** -65, 2.0 ** 65):
             assert f(scale=s) == ERR_UNSUPPORTED, s
         for k in ("X", "t", "n"):
             assert f(**{k: None}) == ERR_NULL, k
