@@ -840,7 +840,7 @@ def _mx4_rows(name: str, codes: torch.Tensor, scale: torch.Tensor, d: Optional[i
     if codes.shape != lead + (16 * B,):
         raise ValueError(f"{name} must have shape {list(lead) + [16 * B]}, got {list(codes.shape)}")
     if d is None:
-        d = 32 * B
+        d = min(32 * B, 131071)  # the widest row
     elif (int(d) + 31) // 32 != B:
         raise ValueError(f"{name} has {B} blocks of 32 in a row, not those of d = {d}")
     return lead, math.prod(lead), int(d), B
@@ -877,7 +877,7 @@ def maxsim_quantize_mx4(X: torch.Tensor, mask: Optional[torch.Tensor] = None,
 def maxsim_dequantize_mx4(codes: torch.Tensor, scale: torch.Tensor, d: Optional[int] = None,
                           out_dtype=torch.bfloat16, Y: Optional[torch.Tensor] = None, stream=None):
     """The values of 4-bit rows: codes [..., 16 B], scale [..., B] to Y [..., d] of
-    ``out_dtype`` (fp16, bf16 or fp32); d is 32 B by default."""
+    ``out_dtype`` (fp16, bf16 or fp32); d is 32 B by default (at most 131071)."""
     lead, T, d, _ = _mx4_rows("codes", codes, scale, d)
     dt = out_dtype if Y is None else Y.dtype
     code = _row_type("out_dtype", dt)
@@ -1007,7 +1007,7 @@ def maxsim_logprob_fwd(X: torch.Tensor, targets: torch.Tensor, mask: Optional[to
                        top_logp: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None, stream=None):
     """Log probabilities of columns ``targets`` [Nq, P] int32 under the softmax of
-    ``scale`` X, rows of scores X [Nq, Nd] (fp16/bf16/fp32), mask uint8 [Nq, Nd].
+    ``scale`` X (2^-64 to 2^64), rows of scores X [Nq, Nd] (fp16/bf16/fp32), mask uint8 [Nq, Nd].
     Returns (logp [Nq, P], rank int32 [Nq, P], norm [Nq, 2], entropy [Nq],
     top_idx int32 [Nq, k], top_logp [Nq, k]; the last two None with k = 0).
     ``workspace`` is uint8 of maxsim_logprob_workspace bytes."""

@@ -398,6 +398,33 @@ def test_scores_without_tokens(ms):
         assert s.shape == (Nq, Nd) and (s == 0).all() and (a == 0).all()
 
 
+def test_scores_of_many_queries(ms):
+    """More queries than one launch takes, of one token and of several tiles."""
+    for Nq, Lq, d in (((1 << 20) + 5, 1, 32), ((1 << 20) + 2, 40, 32)):
+        Q, Qs = _random_mx4((7, Lq), d, 1, 1)  # sums are exact
+        D, Ds = _random_mx4((2, 33), d, 2, 1)
+        want, arg = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, want_argmax=True)
+        of = torch.arange(Nq, device=DEV) % 7
+        qm = torch.ones(Nq, Lq, dtype=torch.uint8, device=DEV)
+        qm[-1] = 0
+        s, a = ms.maxsim_fwd_mx4(Q[of].contiguous(), Qs[of].contiguous(), D, Ds, qm, want_argmax=True)
+        assert torch.equal(s[:-1], want[of][:-1]) and torch.equal(a[:-1], arg[of][:-1])
+        assert (s[-1] == 0).all()
+
+
+def test_widest_rows(ms):
+    """4096 blocks: quantised, multiplied and turned back without naming the width."""
+    d = 131071
+    x = _rows(3, d, torch.bfloat16, 1)
+    codes, scale = ms.maxsim_quantize_mx4(x)
+    assert scale.shape == (3, 4096)
+    y = ms.maxsim_linear_mx4(codes, scale, codes, scale, out_dtype=torch.float32)
+    want, mag = _linear_want(codes, scale, codes, scale, None)
+    _within("product", y, want, ref.linear_bound(want, mag, d, 0.0, torch.float32))
+    back = ms.maxsim_dequantize_mx4(codes, scale, out_dtype=torch.float32)
+    assert torch.equal(back.double(), _values(codes, scale)[:, :d])
+
+
 def test_scores_beyond_32_bit_offsets(ms):
     Nd, Ld, d = 70000, 1000, 128
     D = torch.zeros(Nd, Ld, d // 2, dtype=torch.uint8, device=DEV)
