@@ -35,18 +35,19 @@ FLAGS = [
 
 
 # Per-source additions. The Chamfer kernel's MFMA results feed VALU min
-# updates directly (those of the 4-bit scores max updates), so they go to ordinary VGPRs instead of the
-# accumulation registers (no copy back per MFMA); the other kernels keep the
-# compiler's default register form. The embedding head carries activations and
-# gradients, where an overflow upstream must stay visible: NaNs are honoured
-# there (later flags win), as they are where 4-bit rows mark a NaN by their scale,
-# and in the top-k, which keeps k candidates
-# whatever the scores hold.
+# updates directly, and those of the 4-bit scores max updates, so they go to
+# ordinary VGPRs instead of the accumulation registers (no copy back per MFMA);
+# the other kernels keep the compiler's default register form. The embedding
+# head carries activations and gradients, where an overflow upstream must stay
+# visible: NaNs are honoured there (later flags win), as they are where 4-bit
+# rows mark a NaN by their scale and in the log probabilities. They are in the
+# top-k too, which keeps k candidates whatever the scores hold.
 _NANS = ["-Xarch_device", "-fhonor-nans", "-Xarch_device", "-mamdgpu-ieee"]
 EXTRA = {"chamfer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "topk.hip": _NANS, "embed_rows.hip": _NANS, "embed_linear.hip": _NANS,
          "mx4_rows.hip": _NANS, "mx4_linear.hip": _NANS, "logprob.hip": _NANS,
-         **dict.fromkeys(("fwd_mx4.hip", "fwd_mx4_wide.hip"), _NANS + ["-mllvm", "-amdgpu-mfma-vgpr-form"])}
+         **dict.fromkeys(["fwd_mx4.hip", "fwd_mx4_wide.hip"],
+                         _NANS + ["-mllvm", "-amdgpu-mfma-vgpr-form"])}
 
 
 def _run(cmd, verbose):

@@ -102,6 +102,7 @@ __device__ __forceinline__ void store_run(void* Y, int out, int64_t t, int n, in
             if (n + i < N) p[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
     }
 }
+
 // Four dma_lds16 (NT: with the non-temporal hint) from one base to four KB in a
 // row of LDS; they share the wait states behind the base. Against four single
 // loads, 200,000 x 2048 to 256 channels take 167.7 instead of 181.3 us and

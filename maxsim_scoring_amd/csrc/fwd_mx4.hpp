@@ -23,6 +23,13 @@
 // replaced by zeros and 2^0 (so that a NaN among them is not seen) and the
 // accumulator starts at -inf in their rows. A range's mask becomes bits in LDS
 // first, so that the masked tail of a padded document is not read at all.
+//
+// One query of 32 tokens over 50,000 documents of 180, a quarter masked, 128 channels:
+// 94 us, 468 MB at 5.0 TB/s (without a mask 612 MB at 5.45, the rate of a copy). 32
+// queries over 1000 pages of 1024 tokens: 66 us, 4.1 PFLOP/s of the 4.6 to 5.1 that a
+// loop of these MFMAs alone reaches; 7.5 us for 5 queries over 333 short documents, a
+// launch and a few chains of loads. Loads that bypass the caches were slower (98 us
+// against 94, 256 channels 117 against 71): later chunks of a line come from L1.
 #include "mx4_common.hpp"
 #include "kernels.hpp"
 

@@ -3,23 +3,33 @@
 //
 // Forward. A row is cut into chunks of 4096 columns, one workgroup each, 16 columns
 // a thread in registers, read once: the largest score, the sums of exp(z) and of
-// exp(z) z against it, how many columns come before each target (a ballot and a
-// bit count per register), and the candidates for the best columns. Rows of one
-// chunk (one wave up to 1024 columns) finish there; otherwise a second launch joins
-// the chunks of a row. Few long rows spread over the card in this way.
+// exp(z) z against it, how many columns come before each target, and the candidates
+// for the best columns. Rows of one chunk finish there (those of up to 256 or 512
+// columns in one wave); otherwise a second launch joins the chunks of a row. Few long
+// rows spread over the card in this way.
+//
+// 128 rows of 128 columns, one target, 8 best: 5.2 us. 32 rows of 100,000, 8 targets,
+// 100 best: 14.3 us, and 8.2 us the join of 25 chunks a row. Not the 12.8 MB of
+// scores (2.4 us at a copy's rate) but instructions are the bound: of 14,500 cycles of
+// a workgroup 4,700 count ranks (two instructions for each score and target), 4,900
+// select and copy the best, and 2,000 wait for the scores.
 //
 // The sums take 2^t with t = (x - m) scale log2(e) from the hardware, off by 4 units
 // of 2^-24 |z| for the three roundings of t; they are float64, so that a row whose
 // largest probability is close to 1 keeps its entropy.
 //
 // Best columns. Scores map to 32-bit keys in float order. A histogram of 256 equal
-// bins between the chunk's least and largest key finds the bin of the k-th; it is
-// cut into 256 again only while more than k + k/2 + 32 lie at or above its lower
-// edge. Equal keys that are too many are told apart by their columns in the same
-// way. What is left is ordered by counting, for each, how many are larger.
+// bins between the chunk's least and largest key finds the bin of the k-th: first of
+// the threads' largest keys alone, which seldom leaves many more than k, otherwise of
+// all keys (32 x 100,000 as above: 23.8 us with all keys only, 22.5 us so); it is cut
+// into 256 again only while more than k + k/2 + 32 lie at or above its lower edge.
+// Equal keys that are too many are told apart by their columns in the same way. What
+// is left is ordered by counting, for each, how many are larger.
 //
 // Backward. One pass, element-wise but for the targets: their gradients are added
-// into a chunk of columns in LDS by one wave, in the order of the targets.
+// into a chunk of columns in LDS by one wave, in the order of the targets. 512 rows of
+// 100,000 columns with 32 targets and the entropy's gradient: 410 MB in 79 us, 5.2
+// TB/s; 128 rows of 128 columns: 3.5 us.
 #include "logprob.hpp"
 #include "kernels.hpp"
 
@@ -831,9 +841,10 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
 }
 
 // One wave takes a row of as many columns as one load a lane brings, four waves one of
-// four times as many: where they would have 16 columns a lane, the targets' ranks and
-// the ordering of the best keep a wave busy (16 rows of 752 columns with 32 targets
-// 32 us).
+// four times as many: with 16 columns a lane the targets' ranks and the ordering of
+// the best keep few waves busy (16 rows of 752 columns with 32 targets: one wave of 16
+// columns a lane 32 us, four waves 10.7). Chunks of eight waves with 8 columns a lane
+// are no faster than of four with 16 (32 x 100,000: 15.1 and 14.3 us).
 template <int E>
 void forward(const LogprobArgs& a, hipStream_t stream)
 {

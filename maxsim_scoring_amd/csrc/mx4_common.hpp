@@ -47,7 +47,7 @@ struct Mx4FwdArgs {
     int32_t nb;
     // filled by the launcher
     int32_t ntq;      // 32-token tiles of a query
-    int32_t qpw;      // whole queries of a workgroup
+    int32_t qpw;      // whole queries of a unit
     int32_t nqb;      // blocks of queries
     int32_t nranges;  // ranges of documents
 };
