@@ -841,11 +841,12 @@ def maxsim_dropout_bwd(dY: torch.Tensor, p: float, seed: int, step: int = 0,
 def _mx4_rows(name: str, codes: torch.Tensor, scale: torch.Tensor, d: Optional[int]):
     """(leading shape, rows, width, blocks) of 4-bit rows. Without d the width is
     that of whole blocks."""
-    if codes.dtype != torch.uint8 or scale.dtype != torch.uint8:
+    if codes.dtype is not torch.uint8 or scale.dtype is not torch.uint8:
         raise ValueError(f"{name} and its scale must be uint8")
-    if scale.dim() < 1 or codes.dim() != scale.dim():
+    shape = tuple(scale.shape)
+    if not shape:
         raise ValueError(f"{name} must be [..., 16 B] and its scale [..., B]")
-    lead, B = scale.shape[:-1], scale.shape[-1]
+    lead, B = shape[:-1], shape[-1]
     if codes.shape != lead + (16 * B,):
         raise ValueError(f"{name} must have shape {list(lead) + [16 * B]}, got {list(codes.shape)}")
     if d is None:
