@@ -258,6 +258,14 @@ def test_rows_beyond_32_bit_offsets(ms):
     _close("dX", dX[-2:], want, bound + np.abs(want) * HALF[torch.float16] + FLOOR[torch.float16])
 
 
+@pytest.mark.parametrize("Nd,P,k", [(2200001, 600, 1024), (2200001, 3, 1)])
+def test_long_rows(ms, Nd, P, k):
+    """More chunks, and more targets, than the join has threads."""
+    x, t, mask = _case(1, Nd, P, torch.float32, 3, k > 1)
+    out = _check_forward(ms, x, t, mask, 2.0, k)
+    _check_backward(ms, x, t, mask, 2.0, out, True, torch.float32)
+
+
 def test_many_rows(ms):
     """More rows than one launch takes."""
     Nq = (1 << 22) + 3
