@@ -22,6 +22,7 @@ __global__ __launch_bounds__(256) void zero_mx4_kernel(Mx4FwdArgs a)
 // with 8.
 void scores_once(Mx4FwdArgs a, hipStream_t stream)
 {
+    if (launch_fwd_mx4_short(a, stream) || launch_fwd_mx4_packed(a, stream)) return;
     const int64_t tiles = a.Nq * a.ntq;
     const int64_t most = tiles * a.Nd / ((int64_t)device_cu_count() * 8);
     int n = (int)(most < tiles ? (most > 1 ? most : 1) : tiles);

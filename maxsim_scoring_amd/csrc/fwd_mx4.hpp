@@ -17,7 +17,7 @@
 // unit stay in the caches for the other units of its range, which follow it on the
 // same XCD. Queries of more than NTW tiles are split over the four waves of a
 // workgroup, which leave their sums in LDS to be added in order; otherwise waves share
-// nothing.
+// nothing. Queries of up to 16 tokens share a tile, in slots of a power of two columns.
 //
 // Masked tokens cost nothing per query tile: their codes and exponents are
 // replaced by zeros and 2^0 (so that a NaN among them is not seen) and the
@@ -133,19 +133,31 @@ __device__ __forceinline__ void place_scales(Token<G>& t, int h)
     }
 }
 
-template <int G, int NTW, int P, bool ARGMAX, bool FAST, bool SPLIT>
+// Workgroup b of n runs on XCD b % 8: each XCD takes a run of consecutive units.
+__device__ __forceinline__ int xcd_order(int b, int n)
+{
+    const int full = n >> 3, rem = n & 7, xcd = b & 7;
+    return xcd * full + (xcd < rem ? xcd : rem) + (b >> 3);
+}
+
+// How a query's tokens lie in the unit's tiles.
+enum {
+    kWhole,   // whole queries of one or more tiles each
+    kSplit,   // one query over the waves of a workgroup
+    kPacked,  // queries of up to 16 tokens share tiles, in slots of a power of two
+};
+
+template <int G, int NTW, int P, bool ARGMAX, bool FAST, int MODE>
 __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
 {
+    constexpr bool SPLIT = MODE == kSplit, PACKED = MODE == kPacked;
     __shared__ uint32_t mask_lds[kWaves][kMaskWords];
     __shared__ float part[SPLIT ? kWaves : 1][SPLIT ? kSplitDocs : 1];
 
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id(), col = lane & 31, h = lane >> 5;
     uint32_t* const my_mask = mask_lds[wave];
 
-    // unit of work: XCD-aware order (workgroup b runs on XCD b % 8)
-    const int nblk = gridDim.x, b = blockIdx.x;
-    const int full = nblk >> 3, rem = nblk & 7, xcd = b & 7;
-    const int wg = xcd * full + (xcd < rem ? xcd : rem) + (b >> 3);
+    const int wg = xcd_order(blockIdx.x, gridDim.x);
     const int64_t unit = SPLIT ? wg : (int64_t)wg * kWaves + wave;
     if (unit >= (int64_t)a.nqb * a.nranges) return;  // (the whole workgroup, if SPLIT)
     const int qb = (int)(unit % a.nqb);
@@ -162,6 +174,7 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
     const int i0 = uniform(qb * a.qpw);
     const int nq = uniform((int)(a.Nq - i0 < a.qpw ? a.Nq - i0 : a.qpw));
     const int ntq = a.ntq;
+    const int lq = a.log2_qslot, qpt = 32 >> lq;  // columns of a packed query, queries of a tile
 
     // a split query takes a pass for each kWaves * NTW of its tiles
     for (int q0 = 0; q0 == 0 || (SPLIT && q0 < ntq); q0 += kWaves * NTW) {
@@ -170,17 +183,26 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
         Token<G> q[NTW];
         uint32_t live = 0;  // bit n: this lane's column of tile n exists and counts
         static_for<0, NTW>([&](auto n) {
-            // tile n is tile n % ntq of query n / ntq, or tile first + n of the one query
-            const int qi = SPLIT ? 0 : n / ntq, qt = SPLIT ? first + n : n % ntq;
-            const bool tile_in = qi < nq && qt < ntq;
-            const int64_t i = i0 + (tile_in ? qi : 0);
-            const int t0 = tile_in ? qt * 32 : 0, s = t0 + col;
-            const int row = s < Lq ? col : Lq - 1 - t0;
-            const int64_t tok = i * Lq + t0;
-            load_token<G, FAST, true>(q[n], a.Q + tok * nb * 16, a.q_scale + tok * nb, row, h, nb);
-            place_scales<G, FAST>(q[n], h);
-            const bool on = tile_in && s < Lq && (!a.q_mask || a.q_mask[i * Lq + s]);
-            live |= (uint32_t)on << n;
+            if constexpr (PACKED) {
+                const int qi = n * qpt + (col >> lq), s = col & ((1 << lq) - 1);
+                const int64_t base = (int64_t)i0 * Lq;
+                const int row = (qi < nq ? qi : nq - 1) * Lq + (s < Lq ? s : Lq - 1);
+                load_token<G, FAST, true>(q[n], a.Q + base * nb * 16, a.q_scale + base * nb, row, h, nb);
+                place_scales<G, FAST>(q[n], h);
+                live |= (uint32_t)(qi < nq && s < Lq && (!a.q_mask || a.q_mask[base + row])) << n;
+            } else {
+                // tile n is tile n % ntq of query n / ntq, or tile first + n of the one query
+                const int qi = SPLIT ? 0 : n / ntq, qt = SPLIT ? first + n : n % ntq;
+                const bool tile_in = qi < nq && qt < ntq;
+                const int64_t i = i0 + (tile_in ? qi : 0);
+                const int t0 = tile_in ? qt * 32 : 0, s = t0 + col;
+                const int row = s < Lq ? col : Lq - 1 - t0;
+                const int64_t tok = i * Lq + t0;
+                load_token<G, FAST, true>(q[n], a.Q + tok * nb * 16, a.q_scale + tok * nb, row, h, nb);
+                place_scales<G, FAST>(q[n], h);
+                const bool on = tile_in && s < Lq && (!a.q_mask || a.q_mask[i * Lq + s]);
+                live |= (uint32_t)on << n;
+            }
         });
 
         float m[NTW];
@@ -215,12 +237,18 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                 int i = i0, at = 0;  // the query of tile n, and which of its tiles that is
                 float sums = 0.0f;   // of this lane's columns of the query's tiles so far
                 auto put = [&](int n, int idx) {
-                    const int s = (SPLIT ? first + n : at) * 32 + col;
-                    if (s < Lq) a.argmax[(i * a.Nd + doc) * Lq + s] = idx;
+                    if constexpr (PACKED) {
+                        const int qi = n * qpt + (col >> lq), s = col & ((1 << lq) - 1);
+                        if (qi < nq && s < Lq) a.argmax[((int64_t)(i0 + qi) * a.Nd + doc) * Lq + s] = idx;
+                    } else {
+                        const int s = (SPLIT ? first + n : at) * 32 + col;
+                        if (s < Lq) a.argmax[(i * a.Nd + doc) * Lq + s] = idx;
+                    }
                 };
                 static_for<0, (NTW + 1) / 2>([&](auto pair) {
                     constexpr int n = 2 * pair, n2 = n + 1 < NTW ? n + 1 : n;
-                    if (!SPLIT && i >= i0 + nq) return;
+                    if (PACKED && n * qpt >= nq) return;
+                    if (!SPLIT && !PACKED && i >= i0 + nq) return;
                     if (SPLIT && first + n >= ntq) return;
                     float v;
                     if constexpr (n2 > n) {
@@ -240,12 +268,20 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                             best[k] = o > m[k] || (o == m[k] && oi < best[k]) ? oi : best[k];
                         });
                     }
+                    if constexpr (MODE != kWhole && ARGMAX) {
+                        if (h == 0) put(n, best[n]);
+                        if (n2 > n && h == 0) put(n2, best[n2]);
+                    }
                     if constexpr (SPLIT) {
-                        if constexpr (ARGMAX) {
-                            if (h == 0) put(n, best[n]);
-                            if (n2 > n && h == 0) put(n2, best[n2]);
-                        }
                         sums += v;  // (tiles behind the last one have no column that counts)
+                    } else if constexpr (PACKED) {
+                        if (lq > 0) v = dpp_add<0xB1>(v);   // quad_perm [1,0,3,2]
+                        if (lq > 1) v = dpp_add<0x4E>(v);   // quad_perm [2,3,0,1]
+                        if (lq > 2) v = dpp_add<0x141>(v);  // row_half_mirror
+                        if (lq > 3) v = dpp_add<0x140>(v);  // row_mirror
+                        const int qi = (h ? n2 : n) * qpt + (col >> lq);
+                        if ((col & ((1 << lq) - 1)) == 0 && qi < nq && (n2 > n || h == 0))
+                            a.scores[(int64_t)(i0 + qi) * a.Nd + doc] = v;
                     } else {
                         static_for<n, n2 + 1>([&](auto k) {
                             if (i >= i0 + nq) return;
@@ -408,6 +444,20 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
 
 inline int64_t pieces(int64_t n, int b) { return (n + b - 1) / b; }
 
+inline int log2_up(int64_t n)
+{
+    int l = 0;
+    while (((int64_t)1 << l) < n) ++l;
+    return l;
+}
+
+// The rows that FAST loads take.
+template <int G>
+bool fast_rows(const Mx4FwdArgs& a)
+{
+    return a.nb == 4 * G && (((uintptr_t)a.q_scale | (uintptr_t)a.d_scale) & 3) == 0;
+}
+
 // WAVES: units that a CU runs at once, 4 for each that a SIMD's registers hold, or
 // fewer where more ran slower.
 template <int G, int NTW, int P, int WAVES>
@@ -415,18 +465,19 @@ void run(Mx4FwdArgs a, hipStream_t stream)
 {
     const bool split = a.ntq > NTW;
     a.qpw = split ? 1 : NTW / a.ntq;
+    a.log2_qslot = 5;
     a.nqb = (int32_t)pieces(a.Nq, a.qpw);
     const int64_t units = (int64_t)device_cu_count() * (split ? WAVES / kWaves : WAVES);
     const int64_t want = units / a.nqb > 0 ? units / a.nqb : 1;
     a.nranges = (int32_t)(want < a.Nd ? want : a.Nd);
     const int64_t total = (int64_t)a.nqb * a.nranges;
     const dim3 grid((unsigned)(split ? total : pieces(total, kWaves))), block(kWaves * 64);
-    const bool fast = a.nb == 4 * G && (((uintptr_t)a.q_scale | (uintptr_t)a.d_scale) & 3) == 0;
+    const bool fast = fast_rows<G>(a);
     // (more query registers beside an argmax's would spill)
 #define MAXSIM_MX4_SPLIT(ARGMAX, FAST)                                                                                  \
     do {                                                                                                                \
-        if (split) hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, true>), grid, block, 0, stream, a);      \
-        else hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, false>), grid, block, 0, stream, a);           \
+        if (split) hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, kSplit>), grid, block, 0, stream, a);      \
+        else hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, kWhole>), grid, block, 0, stream, a);           \
     } while (0)
     if constexpr (NTW < 4 || (NTW == 4 && G < 4)) {
         if (a.argmax && fast) MAXSIM_MX4_SPLIT(true, true);

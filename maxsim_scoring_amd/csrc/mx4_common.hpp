@@ -50,6 +50,7 @@ struct Mx4FwdArgs {
     int32_t qpw;      // whole queries of a unit
     int32_t nqb;      // blocks of queries
     int32_t nranges;  // ranges of documents
+    int32_t log2_slot, log2_qslot;  // rows of a short document, columns of a query (5: of a tile)
 };
 
 hipError_t launch_quantize_mx4(int elem, Mx4RowArgs a, bool normalize, hipStream_t stream);
@@ -57,12 +58,17 @@ hipError_t launch_dequantize_mx4(Mx4RowArgs a, hipStream_t stream);
 hipError_t launch_linear_mx4(Mx4LinearArgs a, hipStream_t stream);
 hipError_t launch_fwd_mx4(Mx4FwdArgs a, hipStream_t stream);
 void launch_fwd_mx4_wide(const Mx4FwdArgs& a, int n, hipStream_t stream);
+bool launch_fwd_mx4_short(Mx4FwdArgs a, hipStream_t stream);
+bool launch_fwd_mx4_packed(Mx4FwdArgs a, hipStream_t stream);
 
 // The block-scaled matrix product of 4-bit operands. A lane's 16 bytes are 32
 // codes, one block: lane l of the 32-row form holds row l % 32, block l / 32 of
 // two; of the 16-row form row l % 16, block l / 16 of four. Byte SA (SB) of its
 // scale word is the block's exponent. (The intrinsic takes operands of up to 8
-// bits; with format 4 the upper registers are not read.)
+// bits; with format 4 the upper registers are not read.) The scales are taken from the
+// lanes that EXEC enables, so all lanes have to get here: results that only some
+// lanes use must not be computed where the compiler can move them into those lanes'
+// branch.
 __device__ __forceinline__ i32x8 widen(const i32x4& a) { return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1); }
 template <int SA, int SB>
 __device__ __forceinline__ f32x16 mfma32_mx4(const i32x4& a, int sa, const i32x4& b, int sb, const f32x16& c)

@@ -390,6 +390,36 @@ def test_scores_nan(ms, Nq, Lq, Nd, Ld):
     assert not torch.isnan(s).any()
 
 
+SHORT = [(1, 32, 9, 1, 128), (2, 40, 70, 2, 128), (5, 20, 333, 3, 80), (3, 5, 50, 4, 96), (9, 1, 100, 5, 64), (33, 2, 17, 7, 32),
+         (20, 9, 31, 8, 100), (7, 16, 300, 9, 128), (2, 300, 40, 16, 128), (1, 130, 5, 13, 256), (6, 3, 64, 1, 200), (70, 16, 65, 2, 128),
+         (3, 33, 40, 10, 384), (5, 8, 33, 16, 512), (4, 70, 21, 3, 768), (2, 17, 10, 6, 1024), (40, 4, 2000, 11, 128), (1, 1, 1, 1, 1)]
+
+
+PACKED = [(2, 16, 9, 40, 128), (7, 9, 300, 50, 128), (33, 1, 40, 70, 64), (70, 2, 200, 33, 80), (9, 3, 20, 300, 200), (40, 5, 30, 65, 256),
+          (5, 16, 700, 20, 96), (11, 8, 6, 100, 384), (6, 4, 9, 40, 512), (20, 12, 7, 35, 768), (3, 7, 5, 64, 1000), (200, 6, 60, 90, 128)]
+
+
+@pytest.mark.parametrize("Nq,Lq,Nd,Ld,d", SHORT + PACKED)
+def test_scores_of_short_documents_and_queries(ms, Nq, Lq, Nd, Ld, d):
+    for spread in (1, 5):
+        Q, Qs = _random_mx4((Nq, Lq), d, Lq + d, spread)
+        D, Ds = _random_mx4((Nd, Ld), d, Ld + d, spread)
+        _check_scores(ms, Q, Qs, D, Ds, None, None, d, spread == 1)
+        qm, dm = _mask((Nq, Lq), 1), _mask((Nd, Ld), 2)
+        dm[Nd // 2] = 0                                  # a document without a token
+        qm[Nq // 2] = 0
+        _check_scores(ms, Q, Qs, D, Ds, qm, dm, d, spread == 1)
+    # a NaN block shows in the scores that its token enters, and only there
+    clean, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds)
+    Ds[Nd - 1, Ld - 1, 0] = 255
+    got, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds)
+    assert torch.isnan(got[:, -1]).all() and torch.equal(got[:, :-1], clean[:, :-1])
+    dm = torch.ones(Nd, Ld, dtype=torch.uint8, device=DEV)
+    dm[Nd - 1, Ld - 1] = 0
+    got, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm)
+    assert not torch.isnan(got).any() and torch.equal(got[:, :-1], clean[:, :-1])
+
+
 def test_scores_without_tokens(ms):
     for Nq, Lq, Nd, Ld in ((2, 0, 3, 5), (2, 4, 3, 0), (0, 4, 3, 5), (2, 4, 0, 5), (2, 0, 3, 0)):
         Q, Qs = _random_mx4((Nq, Lq), 64, 1)
