@@ -14,10 +14,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmaxsim_amd.so")
-SOURCES = ["abi.hip", "fwd_dense.hip", "fwd_varlen.hip", "fwd_dim.hip", "bwd.hip", "topk.hip", "chamfer.hip",
+# (those that take longest to compile first)
+SOURCES = ["fwd_mx4_short.hip", "fwd_mx4_wide.hip", "fwd_mx4.hip", "fwd_mx4_packed.hip",
+           "abi.hip", "fwd_dense.hip", "fwd_varlen.hip", "fwd_dim.hip", "bwd.hip", "topk.hip", "chamfer.hip",
            "embed_abi.hip", "embed_rows.hip", "embed_linear.hip",
-           "mx4_abi.hip", "mx4_rows.hip", "mx4_linear.hip", "fwd_mx4.hip", "fwd_mx4_wide.hip",
-           "fwd_mx4_short.hip", "fwd_mx4_packed.hip", "logprob_abi.hip", "logprob.hip"]
+           "mx4_abi.hip", "mx4_rows.hip", "mx4_linear.hip", "logprob_abi.hip", "logprob.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -46,7 +47,8 @@ _NANS = ["-Xarch_device", "-fhonor-nans", "-Xarch_device", "-mamdgpu-ieee"]
 EXTRA = {"chamfer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "topk.hip": _NANS, "embed_rows.hip": _NANS, "embed_linear.hip": _NANS,
          "mx4_rows.hip": _NANS, "mx4_linear.hip": _NANS, "logprob.hip": _NANS,
-         **dict.fromkeys(["fwd_mx4.hip", "fwd_mx4_wide.hip", "fwd_mx4_short.hip", "fwd_mx4_packed.hip"],
+         **dict.fromkeys(["fwd_mx4.hip", "fwd_mx4_wide.hip", "fwd_mx4_short.hip",
+                          "fwd_mx4_packed.hip"],
                          _NANS + ["-mllvm", "-amdgpu-mfma-vgpr-form"])}
 
 

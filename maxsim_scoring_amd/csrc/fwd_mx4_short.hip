@@ -114,48 +114,46 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_short_kernel(Mx4FwdArgs a
                     }
                 }
             };
-            auto fold = [&](auto masked) __attribute__((always_inline)) {
-                const uint32_t mine = bits >> (4 * h);
-                f32x16 start;
+            f32x16 start;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) start[e] = 0.0f;
+            const uint32_t mine = bits >> (4 * h);
+            if (bits != 0xffffffffu) {
+                // codes are finite whatever they are; an exponent may be NaN
+#pragma unroll
+                for (int g = 0; g < G; ++g) s.t.scale[g] = (bits >> col) & 1 ? s.t.scale[g] : 0;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    start[e] = masked && !((mine >> (8 * (e >> 2) + (e & 3))) & 1) ? -__builtin_inff() : 0.0f;
-                if constexpr (masked) {
-                    // codes are finite whatever they are; an exponent may be NaN
-#pragma unroll
-                    for (int g = 0; g < G; ++g) s.t.scale[g] = (bits >> col) & 1 ? s.t.scale[g] : 0;
-                }
-                float sums[NV];
-                static_for<0, NV>([&](auto v) __attribute__((always_inline)) { sums[v] = 0.0f; });
-                int i = i0, at = 0;  // the query, and which of its tiles
-                static_for<0, NTW>([&](auto n) __attribute__((always_inline)) {
-                    if (n >= used) return;
-                    f32x16 acc = start;
-                    static_for<0, G>([&](auto g) {
-                        acc = mfma32_mx4<0, 0>(s.t.code[2 * g], s.t.scale[g], q[n].code[2 * g], q[n].scale[g], acc);
-                        acc = mfma32_mx4<1, 1>(s.t.code[2 * g + 1], s.t.scale[g], q[n].code[2 * g + 1], q[n].scale[g], acc);
-                    });
-                    // What does not count is masked off in bits: with a condition in its place the
-                    // MFMAs were moved into a branch of the lanes that count, and needed the scales
-                    // of all.
-                    const uint32_t counts = 0u - ((live >> n) & 1);
-                    static_for<0, NV>([&](auto v) __attribute__((always_inline)) {
-                        float m = acc[v * S];
-                        static_for<1, S>([&](auto e) __attribute__((always_inline)) { m = vmax(m, acc[v * S + e]); });
-                        uint32_t keep = counts;  // (a document without a token that counts scores 0)
-                        if constexpr (masked) keep &= 0u - (uint32_t)((mine & rows_of<LS>(v)) != 0);
-                        sums[v] += as_float(__builtin_bit_cast(uint32_t, m) & keep);
-                    });
-                    if (qpt > 1 || ++at == ntq || n + 1 == used) {
-                        flush(sums, i);
-                        i += qpt;
-                        at = 0;
-                        static_for<0, NV>([&](auto v) __attribute__((always_inline)) { sums[v] = 0.0f; });
-                    }
+                    start[e] = (mine >> (8 * (e >> 2) + (e & 3))) & 1 ? 0.0f : -__builtin_inff();
+            }
+            float sums[NV];
+            static_for<0, NV>([&](auto v) __attribute__((always_inline)) { sums[v] = 0.0f; });
+            int i = i0, at = 0;  // the query, and which of its tiles
+            static_for<0, NTW>([&](auto n) __attribute__((always_inline)) {
+                if (n >= used) return;
+                f32x16 acc = start;
+                static_for<0, G>([&](auto g) {
+                    acc = mfma32_mx4<0, 0>(s.t.code[2 * g], s.t.scale[g], q[n].code[2 * g], q[n].scale[g], acc);
+                    acc = mfma32_mx4<1, 1>(s.t.code[2 * g + 1], s.t.scale[g], q[n].code[2 * g + 1], q[n].scale[g], acc);
                 });
-            };
-            if (bits == 0xffffffffu) fold(std::false_type{});
-            else fold(std::true_type{});
+                // What does not count is masked off in bits: with a condition in its place the
+                // MFMAs were moved into a branch of the lanes that count, and needed the scales
+                // of all.
+                const uint32_t counts = 0u - ((live >> n) & 1);
+                static_for<0, NV>([&](auto v) __attribute__((always_inline)) {
+                    float m = acc[v * S];
+                    static_for<1, S>([&](auto e) __attribute__((always_inline)) { m = vmax(m, acc[v * S + e]); });
+                    // (a document without a token that counts scores 0)
+                    const uint32_t keep = counts & (0u - (uint32_t)((mine & rows_of<LS>(v)) != 0));
+                    sums[v] += as_float(__builtin_bit_cast(uint32_t, m) & keep);
+                });
+                if (qpt > 1 || ++at == ntq || n + 1 == used) {
+                    flush(sums, i);
+                    i += qpt;
+                    at = 0;
+                    static_for<0, NV>([&](auto v) __attribute__((always_inline)) { sums[v] = 0.0f; });
+                }
+            });
         };
 
         static_for<0, P>([&](auto p) __attribute__((always_inline)) {
@@ -184,8 +182,13 @@ void run_short(Mx4FwdArgs a, hipStream_t stream)
     const bool fast = fast_rows<G>(a);
     auto launch = [&](auto log2_slot) {
         constexpr int LS = log2_slot;
-        if (fast) hipLaunchKernelGGL((fwd_mx4_short_kernel<G, NTW, P, LS, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((fwd_mx4_short_kernel<G, NTW, P, LS, false>), grid, block, 0, stream, a);
+        if constexpr (G == 1) {  // (wider tokens: little of their time)
+            if (fast) {
+                hipLaunchKernelGGL((fwd_mx4_short_kernel<G, NTW, P, LS, true>), grid, block, 0, stream, a);
+                return;
+            }
+        }
+        hipLaunchKernelGGL((fwd_mx4_short_kernel<G, NTW, P, LS, false>), grid, block, 0, stream, a);
     };
     if (a.log2_slot == 4) launch(std::integral_constant<int, 4>{});
     else if (a.log2_slot == 3) launch(std::integral_constant<int, 3>{});
