@@ -15,10 +15,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmaxsim_amd.so")
 # (those that take longest to compile first)
-SOURCES = ["fwd_mx4_short.hip", "fwd_mx4_wide.hip", "fwd_mx4.hip", "fwd_mx4_packed.hip",
-           "abi.hip", "fwd_dense.hip", "fwd_varlen.hip", "fwd_dim.hip", "bwd.hip", "topk.hip", "chamfer.hip",
-           "embed_abi.hip", "embed_rows.hip", "embed_linear.hip",
-           "mx4_abi.hip", "mx4_rows.hip", "mx4_linear.hip", "logprob_abi.hip", "logprob.hip"]
+SOURCES = ["embed_linear.hip", "fwd_mx4_wide.hip", "fwd_mx4_short.hip", "fwd_mx4.hip",
+           "fwd_mx4_packed.hip", "abi.hip", "fwd_dense.hip", "fwd_varlen.hip", "fwd_dim.hip", "bwd.hip", "topk.hip", "chamfer.hip",
+           "embed_abi.hip", "embed_rows.hip", "mx4_abi.hip", "mx4_rows.hip", "mx4_linear.hip",
+           "logprob_abi.hip", "logprob.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
