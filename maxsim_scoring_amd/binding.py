@@ -849,6 +849,8 @@ def _mx4_rows(name: str, codes: torch.Tensor, scale: torch.Tensor, d: Optional[i
     lead, B = shape[:-1], shape[-1]
     if codes.shape != lead + (16 * B,):
         raise ValueError(f"{name} must have shape {list(lead) + [16 * B]}, got {list(codes.shape)}")
+    if B > 4096:
+        raise ValueError(f"{name} has {B} blocks of 32 in a row, 4096 are the most")
     if d is None:
         d = min(32 * B, 131071)  # the widest row
     elif (int(d) + 31) // 32 != B:

@@ -172,6 +172,19 @@ def test_binding_refuses_cpu_tensors():
             call()
 
 
+def test_binding_refuses_rows_of_more_blocks_than_the_widest():
+    """Without a width the blocks say it: those of 4096 make 131071 values, more are no
+    row that the library has. (They were taken as rows of 4096, read at the wrong places.)"""
+    import maxsim_scoring_amd as ms
+    for B, fine in ((4096, True), (4097, False), (5000, False)):
+        u, s = torch.zeros(2, 16 * B, dtype=torch.uint8), torch.zeros(2, B, dtype=torch.uint8)
+        for call in (lambda: ms.maxsim_dequantize_mx4(u, s),
+                     lambda: ms.maxsim_linear_mx4(u, s, u, s),
+                     lambda: ms.maxsim_fwd_mx4(u[None], s[None], u[None], s[None])):
+            with pytest.raises(ValueError, match="GPU tensor" if fine else f"{B} blocks"):
+                call()
+
+
 def test_reference_codes_by_hand():
     row = [[0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.9, -0.3] + [0.0] * 21 + [4.0]]
     code, scale = ref.quantize(row)
