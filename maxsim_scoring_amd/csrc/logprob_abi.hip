@@ -10,7 +10,7 @@ using namespace maxsim;
 
 namespace {
 
-constexpr int64_t kMax = (int64_t)INT32_MAX - kLpChunk;
+constexpr int64_t kMax = ((int64_t)1 << 31) - kLpChunk;  // the end of a row's last chunk stays below 2^31
 constexpr int64_t kI32Max = INT32_MAX;
 
 maxsim_status_t launch_status(hipError_t e) { return e == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_LAUNCH; }

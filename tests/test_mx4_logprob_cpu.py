@@ -157,6 +157,15 @@ def test_logprob_workspace(L):
         assert f(*bad) == -1, bad
 
 
+def test_logprob_largest_sizes(L):
+    """The header's limit itself: 2^31 - 4097 is the largest size, 2^31 - 4096 is refused."""
+    f, most = L.maxsim_logprob_workspace, (1 << 31) - 4097
+    for fine in ((1, most, 1, 1), (1, 5000, most, 1), (most, 5, 0, 0)):
+        assert f(*fine) >= 0, fine
+    for bad in ((1, most + 1, 1, 1), (1, 5000, most + 1, 1), (most + 1, 5, 0, 0)):
+        assert f(*bad) == -1, bad
+
+
 def test_binding_refuses_cpu_tensors():
     import maxsim_scoring_amd as ms
     x, u = torch.zeros(4, 64), torch.zeros(4, 32, dtype=torch.uint8)
