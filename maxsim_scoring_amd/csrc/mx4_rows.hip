@@ -333,6 +333,9 @@ __global__ __launch_bounds__(kThreads) void quantize_mx4_norm_long_kernel(Mx4Row
                 e = exact_exp(n, m);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w |= code_of((double)x[i] / n, e) << (4 * i);
+            } else {  // zeros, which keep their signs (or a row marked NaN: any codes)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w |= (__builtin_bit_cast(uint32_t, x[i]) >> 31) << (4 * i + 3);
             }
             put8(a, row, u, w, odd ? kNanScale : e + 127);
         }

@@ -123,6 +123,22 @@ def test_quantize_borders(ms):
     assert (codes == 0x88).all() and (scale == 127).all()
 
 
+@pytest.mark.parametrize("d", [100, 4096, 8192, 9001, 16640])
+def test_quantize_normalized_zeros_keep_their_sign(ms, d):
+    """Blocks of zeros beside a block that is not, a row of zeros, and a row too small to have a direction."""
+    x = torch.zeros(4, d, device=DEV)
+    x[0, 0], x[0, 1::2] = 3.0, -0.0
+    x[1] = -0.0
+    x[2, ::3] = -2.0 ** -120
+    x[3, 1], x[3, 2:] = -2.0, -0.0
+    codes, scale = ms.maxsim_quantize_mx4(x, normalize=True)
+    n = torch.stack([codes & 15, codes >> 4], -1).view(4, -1)[:, :d]
+    want = torch.signbit(x).to(torch.uint8) * 8
+    assert torch.equal(n[1:3], want[1:3]) and (scale[1:3] == 127).all()
+    assert torch.equal(n[0, 1:], want[0, 1:]) and torch.equal(n[3, 2:], want[3, 2:])
+    assert int(n[0, 0]) == 6 and int(n[3, 1]) == 14 and (scale[:, 1:] == 127).all()
+
+
 def test_quantize_normalized_ties(ms):
     """Rows whose norm is a whole number put values exactly on borders and powers of two."""
     rows = np.zeros((8, 64))
