@@ -230,6 +230,14 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                 __builtin_amdgcn_wave_barrier();
             }
 
+            auto first_token = [&](int doc) {  // that counts, 0 if none does
+                for (int t0 = 0; t0 < Ld; t0 += 64) {
+                    const uint64_t some = __ballot(lane < Ld - t0 && a.d_mask[(int64_t)doc * Ld + t0 + lane]);
+                    if (some) return t0 + __builtin_ctzll(some);
+                }
+                return 0;
+            };
+
             // Sums of a finished document, tiles in order. Both halves of a wave hold the
             // maxima of 32 columns, over different rows: the halves of two tiles are swapped so
             // that one maximum joins both, the first tile's in the low half.
@@ -258,6 +266,7 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                     } else {
                         v = vmax(m[n], shfl_xor_f(m[n], 32));
                     }
+                    const bool lost = ARGMAX && v == -__builtin_inff();
                     const bool mine = (live >> (n2 > n && h ? n2 : n)) & 1;
                     v = any && mine && (n2 > n || h == 0) ? v : 0.0f;
                     if constexpr (ARGMAX) {
@@ -267,6 +276,13 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                             const int oi = shfl_xor_i(best[k], 32);
                             best[k] = o > m[k] || (o == m[k] && oi < best[k]) ? oi : best[k];
                         });
+                        // where all that count are at -inf (products that overflow), the first of them
+                        if (__builtin_expect(__any(lost), 0)) {
+                            const int first = a.d_mask ? first_token(doc) : 0;
+                            static_for<n, n2 + 1>([&](auto k) {
+                                best[k] = vmax(shfl_xor_f(m[k], 32), m[k]) == -__builtin_inff() ? first : best[k];
+                            });
+                        }
                     }
                     if constexpr (MODE != kWhole && ARGMAX) {
                         if (h == 0) put(n, best[n]);

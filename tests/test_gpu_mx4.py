@@ -436,6 +436,30 @@ def test_scores_of_short_documents_and_queries(ms, Nq, Lq, Nd, Ld, d):
     assert not torch.isnan(got).any() and torch.equal(got[:, :-1], clean[:, :-1])
 
 
+@pytest.mark.parametrize("Nq,Lq", [(1, 32), (3, 20), (9, 3), (2, 300)])
+def test_argmax_of_similarities_that_overflow(ms, Nq, Lq):
+    """Where every token that counts is at -Inf, the argmax is the first of them, not a masked one."""
+    d, Nd, Ld = 128, 5, 70
+    Q, Qs = torch.full((Nq, Lq, d // 2), 0x77, dtype=torch.uint8, device=DEV), torch.full((Nq, Lq, d // 32), 254, dtype=torch.uint8, device=DEV)
+    D, Ds = torch.full((Nd, Ld, d // 2), 0xff, dtype=torch.uint8, device=DEV), torch.full((Nd, Ld, d // 32), 254, dtype=torch.uint8, device=DEV)
+    dm = torch.ones(Nd, Ld, dtype=torch.uint8, device=DEV)
+    first = [0, 5, 18, 45, 69]
+    for j, t in enumerate(first):
+        dm[j, :t] = 0
+    dm[1, 6:40] = 0
+    s, a = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm, want_argmax=True)
+    assert (s == -float("inf")).all()
+    assert torch.equal(a, torch.tensor(first, dtype=torch.int32, device=DEV)[None, :, None].expand(Nq, Nd, Lq))
+    Ds[2, 60] = 100  # a finite one is larger
+    Ds[4, 3] = 1     # but does not count
+    s, a = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm, want_argmax=True)
+    first[2] = 60
+    assert torch.equal(a, torch.tensor(first, dtype=torch.int32, device=DEV)[None, :, None].expand(Nq, Nd, Lq))
+    want = -36.0 * d * 2.0 ** (127 + 100 - 127) * Lq
+    assert torch.allclose(s[:, 2].double(), torch.full((Nq,), want, dtype=torch.float64, device=DEV), rtol=1e-5, atol=0)
+    assert (s[:, [0, 1, 3, 4]] == -float("inf")).all()
+
+
 def test_scores_without_tokens(ms):
     for Nq, Lq, Nd, Ld in ((2, 0, 3, 5), (2, 4, 3, 0), (0, 4, 3, 5), (2, 4, 0, 5), (2, 0, 3, 0)):
         Q, Qs = _random_mx4((Nq, Lq), 64, 1)
