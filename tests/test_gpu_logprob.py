@@ -168,6 +168,42 @@ def test_peaked_rows_keep_their_entropy(ms):
             assert np.allclose(_np(got), exact, rtol=1e-5, atol=2.0 ** -52)
 
 
+@pytest.mark.parametrize("Nd", [100, 800, 6000])
+def test_peaked_rows_keep_their_gradient(ms, Nd):
+    """The gradient of a column whose probability is next to 1 is the small rest too:
+    A (1 - p) - p (R + gH (log p + H)), A the gradients that name it, R the others'.
+    With s = (Nd - 1) exp(z) the rest is s / (1 + s). s is off by 4 |z| + 6 units (u = 2^-24),
+    and 34 are for L, H and the sums rounded to 32 bits, the exponential and the products.
+    1 + s is a float64 sum whose partial sums pass 1: 15 additions in the thread that holds
+    the 1, 6 over its wave, 3 over the waves, and 1 + 6 + 7 where chunks are joined, 38 in
+    all, each off by 2^-53 of 1 at most: less than 2^-47."""
+    u = 2.0 ** -24
+    for scale, tops in ((1.0, (20.0, 30.0, 60.0)), (2.0, (8.0, 12.0, 17.0))):
+        for case in range(3):
+            x = torch.zeros(3, Nd, device=DEV)
+            at = [7, Nd - 1, 50]
+            for i in range(3):
+                x[i, at[i]] = tops[i]
+            # the sure column alone; named twice; beside another one, with the entropy
+            names = [[[c] for c in at], [[c, c] for c in at], [[c, 3] for c in at]][case]
+            t = torch.tensor(names, dtype=torch.int32, device=DEV)
+            g = torch.tensor([[1.0], [0.7, 0.45], [1.5, -1e-7]][case], device=DEV).expand(3, -1).contiguous()
+            gh = torch.full((3,), 0.3, device=DEV) if case == 2 else None
+            out = ms.maxsim_logprob_fwd(x, t, scale=scale)
+            dX = _np(ms.maxsim_logprob_bwd(x, t, out[2], g, scale=scale, entropy=out[3] if case == 2 else None, grad_entropy=gh))
+            gs = _np(g)[0]
+            A, R, h = (gs.sum(), 0.0, 0.0) if case < 2 else (gs[0], gs[1], float(gh[0]))
+            for i in range(3):
+                z = -scale * tops[i]
+                s = (Nd - 1) * np.exp(z)
+                L = np.log1p(s)
+                parts = np.array([A * s / (1 + s), -R / (1 + s), -h * (-s * z / (1 + s)) / (1 + s)])  # log p + H = -s z / (1 + s)
+                rtol = 1.01 * u * (4 * abs(z) + 40)
+                assert abs(dX[i, at[i]] - scale * parts.sum()) <= scale * (rtol * np.abs(parts).sum() + 2.0 ** -47 * (A + 100 * h)), (case, i)
+                # the columns' gradients cancel
+                assert abs(dX[i].sum()) <= rtol * np.abs(dX[i]).sum() + scale * 2.0 ** -47 * (A + 100 * h), (case, i)
+
+
 def _random_shape(seed):
     r = np.random.default_rng(seed)
     Nd = int(np.exp(r.uniform(0, np.log(60000))))
