@@ -412,6 +412,7 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                             acc = mfma32_mx4<0, 0>(s.t.code[2 * g], s.t.scale[g], q[n].code[2 * g], q[n].scale[g], acc);
                             acc = mfma32_mx4<1, 1>(s.t.code[2 * g + 1], s.t.scale[g], q[n].code[2 * g + 1], q[n].scale[g], acc);
                         });
+                        stay(acc);
                         if constexpr (!ARGMAX) {
                             m[n] = max16(acc, m[n]);
                         } else {

@@ -137,9 +137,8 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_short_kernel(Mx4FwdArgs a
                     acc = mfma32_mx4<0, 0>(s.t.code[2 * g], s.t.scale[g], q[n].code[2 * g], q[n].scale[g], acc);
                     acc = mfma32_mx4<1, 1>(s.t.code[2 * g + 1], s.t.scale[g], q[n].code[2 * g + 1], q[n].scale[g], acc);
                 });
-                // What does not count is masked off in bits: with a condition in its place the
-                // MFMAs were moved into a branch of the lanes that count, and needed the scales
-                // of all.
+                stay(acc);
+                // what does not count is masked off in bits: no lane branches
                 const uint32_t counts = 0u - ((live >> n) & 1);
                 static_for<0, NV>([&](auto v) __attribute__((always_inline)) {
                     float m = acc[v * S];

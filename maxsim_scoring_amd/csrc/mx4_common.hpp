@@ -66,15 +66,18 @@ bool launch_fwd_mx4_packed(Mx4FwdArgs a, hipStream_t stream);
 // two; of the 16-row form row l % 16, block l / 16 of four. Byte SA (SB) of its
 // scale word is the block's exponent. (The intrinsic takes operands of up to 8
 // bits; with format 4 the upper registers are not read.) The scales are taken from the
-// lanes that EXEC enables, so all lanes have to get here: results that only some
-// lanes use must not be computed where the compiler can move them into those lanes'
-// branch.
+// lanes that EXEC enables, so all lanes have to get here. The compiler does not know
+// that: a result that only some lanes use it computes in those lanes' branch, so one
+// that may be used so is told to stay. (Sums that go round a loop cannot be moved out
+// of it.)
 __device__ __forceinline__ i32x8 widen(const i32x4& a) { return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1); }
 template <int SA, int SB>
 __device__ __forceinline__ f32x16 mfma32_mx4(const i32x4& a, int sa, const i32x4& b, int sb, const f32x16& c)
 {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), widen(b), c, 4, 4, SA, sa, SB, sb);
 }
+// Behind the last of a result's products: it is there before the lanes part.
+__device__ __forceinline__ void stay(f32x16& acc) { asm volatile("" : "+v"(acc)); }
 template <int SA, int SB>
 __device__ __forceinline__ f32x4 mfma16_mx4(const i32x4& a, int sa, const i32x4& b, int sb, const f32x4& c)
 {
