@@ -436,6 +436,27 @@ def test_scores_of_short_documents_and_queries(ms, Nq, Lq, Nd, Ld, d):
     assert not torch.isnan(got).any() and torch.equal(got[:, :-1], clean[:, :-1])
 
 
+@pytest.mark.parametrize("Nq,Lq,Nd,Ld,d", [(1, 32, 9, 70, 128), (9, 40, 6, 70, 100), (9, 3, 40, 40, 256), (2, 300, 5, 90, 128),
+                                          (7, 16, 300, 9, 128), (40, 20, 300, 3, 200), (3, 20, 5, 17000, 64)])
+def test_masked_tokens_beside_the_largest_exponents(ms, Nq, Lq, Nd, Ld, d):
+    """Masked documents' tokens may hold anything: with the largest finite exponents, or
+    NaN, beside queries of the largest ones, scores are those of harmless tokens."""
+    Q, Qs = _random_mx4((Nq, Lq), d, 1, 1)
+    Qs += 134  # 2^127
+    D, Ds = _random_mx4((Nd, Ld), d, 2, 3)
+    Ds -= 60   # 2^-67 and more, so that scores fit: 36 x 256 channels x 300 tokens x 2^60 x 2^3
+    dm = _mask((Nd, Ld), 3, 0.6)
+    dm[0] = 0
+    _check_scores(ms, Q, Qs, D, Ds, None, dm, d, False)
+    clean, arg = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm, want_argmax=True)
+    for top in (254, 255):
+        dirty = torch.where(dm[..., None] == 0, torch.tensor(top, dtype=torch.uint8, device=DEV), Ds)
+        s, a = ms.maxsim_fwd_mx4(Q, Qs, D, dirty, None, dm, want_argmax=True)
+        plain, _ = ms.maxsim_fwd_mx4(Q, Qs, D, dirty, None, dm)
+        assert torch.equal(s, clean) and torch.equal(a, arg)
+        assert torch.equal(plain, ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm)[0])
+
+
 @pytest.mark.parametrize("Nq,Lq", [(1, 32), (3, 20), (9, 3), (2, 300)])
 def test_argmax_of_similarities_that_overflow(ms, Nq, Lq):
     """Where every token that counts is at -Inf, the argmax is the first of them, not a masked one."""
