@@ -284,6 +284,47 @@ def test_linear_large_tiles(ms, T, N, K):
     _within("fp32", got, want, ref.linear_bound(want, mag, K, 0.0, torch.float32))
 
 
+# Where 32 x 16 tiles are more than the CUs: 64 x 64 tiles with a ring of four steps, refilled
+# from five steps on; 128 x 128 tiles, several a workgroup; 256 x 256 tiles. Steps of 8
+# blocks and a rest, whole words of exponents (a multiple of 4 blocks) or not, outputs in rows
+# that 16 bytes divide, that 8 divide, and that they don't.
+TILES_64 = [(700, 600, K) for K in (100, 128, 256, 384, 1000, 1280, 1568, 2176, 2300)] + [(700, 601, 1280), (650, 604, 640)]
+TILES_128 = [(2600, 4096, K) for K in (128, 256, 384, 512, 768, 1152, 1500)] + [(2600, 4099, 512), (2600, 4100, 640), (2560, 4096, 1024),
+                                                                               (2050, 2100, 512)]
+TILES_256 = [(4096, 4100, K) for K in (128, 512, 640, 1152)] + [(4000, 4096, 768), (4096, 4099, 512)]
+
+
+@pytest.mark.parametrize("T,N,K", TILES_64 + TILES_128 + TILES_256)
+def test_linear_of_every_tile(ms, T, N, K):
+    test_linear(ms, T, N, K)
+
+
+@pytest.mark.parametrize("T,N,K", [(700, 600, 1280), (2600, 4096, 512), (4096, 4100, 320)])
+def test_linear_of_tiles_nan_and_overflow(ms, T, N, K):
+    """NaN blocks give NaN rows and channels, products beyond the floats infinities of their
+    sign, and neither reaches the others."""
+    A, As = _random_mx4((T,), K, 1)
+    W, Ws = _random_mx4((N,), K, 2)
+    clean = ms.maxsim_linear_mx4(A, As, W, Ws, out_dtype=torch.float32)
+    at, ch = [1, T // 2, T - 1], [0, N // 2, N - 1]
+    for t, n in zip(at, ch):
+        As[t, K // 32 - 1] = 255
+        Ws[n, 1] = 255
+    A[5], As[5] = 0x77, 254
+    W[6], Ws[6] = 0x77, 254
+    W[7], Ws[7] = 0xff, 254
+    y = ms.maxsim_linear_mx4(A, As, W, Ws, out_dtype=torch.float32)
+    assert torch.isnan(y[at]).all() and torch.isnan(y[:, ch]).all()
+    assert y[5, 6] == float("inf") and y[5, 7] == -float("inf")
+    rows, cols = torch.ones(T, dtype=torch.bool, device=DEV), torch.ones(N, dtype=torch.bool, device=DEV)
+    rows[at + [5]] = False
+    cols[ch + [6, 7]] = False
+    assert torch.equal(y[rows][:, cols], clean[rows][:, cols])
+    for _ in range(3):
+        z = ms.maxsim_linear_mx4(A, As, W, Ws, out_dtype=torch.float32)
+        assert torch.equal(torch.nan_to_num(z, nan=7.0), torch.nan_to_num(y, nan=7.0))
+
+
 @pytest.mark.parametrize("T", [3, 40, 300])
 def test_linear_nan_blocks_and_far_exponents(ms, T):
     K, N = 200, 70
@@ -479,6 +520,83 @@ def test_argmax_of_similarities_that_overflow(ms, Nq, Lq):
     want = -36.0 * d * 2.0 ** (127 + 100 - 127) * Lq
     assert torch.allclose(s[:, 2].double(), torch.full((Nq,), want, dtype=torch.float64, device=DEV), rtol=1e-5, atol=0)
     assert (s[:, [0, 1, 3, 4]] == -float("inf")).all()
+
+
+def _cus():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def _up(n, b):
+    return -(-n // b)
+
+
+def _log2_up(n):
+    return (n - 1).bit_length()
+
+
+def _check_many_scores(ms, Nq, Lq, Nd, Ld, d, seed):
+    """Without and with masks, aligned exponents and others; one exponent, where no sum
+    rounds, if the largest possible score is below 2^24 quarters."""
+    for spread in (1, 5):
+        Q, Qs = _random_mx4((Nq, Lq), d, seed, spread)
+        D, Ds = _random_mx4((Nd, Ld), d, seed + 1, spread)
+        exact = spread == 1 and Lq * d * 144 < 1 << 24
+        _check_scores(ms, Q, Qs, D, Ds, None, None, d, exact)
+        qm, dm = _mask((Nq, Lq), 1), _mask((Nd, Ld), 2)
+        dm[Nd // 2] = 0
+        dm[-1] = 0
+        dm[-1, -1] = 1
+        qm[Nq // 2] = 0
+        _check_scores(ms, Q, Qs, D, Ds, qm, dm, d, exact)
+    s, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, qm, dm)
+    t, _ = ms.maxsim_fwd_mx4(Q, _off_by_one(Qs), D, _off_by_one(Ds), _off_by_one(qm), _off_by_one(dm))
+    assert torch.equal(s, t)
+    want, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds)
+    Ds[Nd - 1, Ld - 1, 0] = 255
+    got, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds)
+    assert torch.isnan(got[:, -1]).all() and torch.equal(got[:, :-1], want[:, :-1])
+    dm = torch.ones(Nd, Ld, dtype=torch.uint8, device=DEV)
+    dm[-1, -1] = 0
+    got, _ = ms.maxsim_fwd_mx4(Q, Qs, D, Ds, None, dm)
+    assert not torch.isnan(got).any() and torch.equal(got[:, :-1], want[:, :-1])
+
+
+# Documents of up to 16 tokens share a tile where there are as many tiles as CUs, several
+# query tiles a wave where there are 16 times as many. (Nq, Lq, whether many): queries that
+# share tiles, of one tile, of two and three in one unit, of more than a unit holds; counts
+# that units do not divide.
+SHORT_QUERIES = [(1, 32, False), (3, 40, False), (20, 3, False), (1, 300, False), (70, 5, True), (9, 20, True), (7, 40, True),
+                 (11, 70, True), (5, 300, True), (200, 1, True)]
+
+
+@pytest.mark.parametrize("Nq,Lq,many", SHORT_QUERIES)
+@pytest.mark.parametrize("d", [128, 96, 256, 200, 512, 1000])
+@pytest.mark.parametrize("Ld", [1, 2, 3, 7, 16])
+def test_scores_of_documents_that_share_tiles(ms, Ld, d, Nq, Lq, many):
+    per = 32 >> _log2_up(Ld)
+    tiles = Nq * _up(Lq, 32) if Lq > 32 else Nq if Lq > 16 else _up(Nq, 32 >> _log2_up(Lq))
+    Nd = _up((16 if many else 1) * _cus(), tiles) * per + (1 if per > 1 else 0)
+    _check_many_scores(ms, Nq, Lq, Nd, Ld, d, Ld + d)
+
+
+# Queries of up to 16 tokens share tiles; four (two above 768 channels) tiles a wave where
+# tiles times documents are 16 for each CU.
+@pytest.mark.parametrize("Nq,Lq,many", [(200, 1, True), (70, 3, True), (39, 8, True), (13, 16, True), (5, 16, False), (40, 3, False)])
+@pytest.mark.parametrize("d", [128, 80, 256, 200, 384, 300, 512, 768, 640, 1024, 1000])
+def test_scores_of_queries_that_share_tiles(ms, d, Nq, Lq, many):
+    tiles = _up(Nq, 32 >> _log2_up(Lq))
+    Nd = _up(16 * _cus(), tiles) + 3 if many else 40
+    _check_many_scores(ms, Nq, Lq, Nd, 33, d, d + Lq)
+
+
+# Whole queries: as many tiles a wave, up to 8, as leave 8 documents' worth for each CU.
+# (Nq, Lq, tiles a wave): one to three tiles a query, counts that units do not divide, and
+# queries split over a workgroup's waves.
+@pytest.mark.parametrize("Nq,Lq,n", [(11, 32, 8), (5, 40, 8), (5, 70, 8), (2, 300, 8), (11, 20, 4), (5, 40, 4), (3, 32, 2), (2, 130, 4)])
+@pytest.mark.parametrize("d", [128, 100, 256, 200, 384, 512, 768, 1024])
+def test_scores_of_several_queries_a_wave(ms, d, Nq, Lq, n):
+    Nd = _up(n * 8 * _cus(), Nq * _up(Lq, 32)) + 1
+    _check_many_scores(ms, Nq, Lq, Nd, 33 if Lq < 100 else 20, d, d + Lq)
 
 
 def test_scores_without_tokens(ms):
