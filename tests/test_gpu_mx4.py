@@ -102,6 +102,13 @@ def test_quantize(ms, T, d, dtype):
                                                       normalize))
 
 
+@by_type
+@pytest.mark.parametrize("T,d", [(9, 205), (9, 300), (9, 384), (5, 1600), (3, 8190)])
+def test_quantize_more_widths(ms, T, d, dtype):
+    """Widths of every number of lanes and units, whole eights of values and others."""
+    test_quantize(ms, T, d, dtype)
+
+
 def test_quantize_borders(ms):
     """Every border between levels, the values next to it, and the powers of two, at exponents over the whole range."""
     base = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.999999, 0.5, 1, 2, 3, 4, 0.0], dtype=np.float32)
@@ -597,6 +604,13 @@ def test_scores_of_queries_that_share_tiles(ms, d, Nq, Lq, many):
 def test_scores_of_several_queries_a_wave(ms, d, Nq, Lq, n):
     Nd = _up(n * 8 * _cus(), Nq * _up(Lq, 32)) + 1
     _check_many_scores(ms, Nq, Lq, Nd, 33 if Lq < 100 else 20, d, d + Lq)
+
+
+# Little work: as few tiles a wave as the query's length leaves.
+@pytest.mark.parametrize("Nq,Lq", [(1, 20), (2, 40), (1, 70), (1, 160), (2, 300), (2, 3), (3, 16)])
+@pytest.mark.parametrize("d", [128, 100, 256, 200, 384, 300, 512, 500, 768, 700, 1024, 1000])
+def test_scores_of_little_work(ms, d, Nq, Lq):
+    _check_many_scores(ms, Nq, Lq, 5, 40, d, d + Lq)
 
 
 def test_scores_without_tokens(ms):
