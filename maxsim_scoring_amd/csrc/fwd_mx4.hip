@@ -35,7 +35,7 @@ void scores_once(Mx4FwdArgs a, hipStream_t stream)
         if (n >= 8 && !a.argmax) run<1, 8, 2, 8>(a, stream);
         else if (n >= 3) run<1, 4, 2, 16>(a, stream);
         else if (n == 2) run<1, 2, 4, 12>(a, stream);
-        else run<1, 1, 4, 20>(a, stream);
+        else run<1, 1, 4, 20, true>(a, stream);
     } else {
         if (n >= 3) run<2, 4, 2, 8>(a, stream);
         else run<2, 1, 3, 8>(a, stream);

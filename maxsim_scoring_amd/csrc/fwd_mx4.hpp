@@ -478,11 +478,12 @@ bool fast_rows(const Mx4FwdArgs& a)
 }
 
 // WAVES: units that a CU runs at once, 4 for each that a SIMD's registers hold, or
-// fewer where more ran slower.
-template <int G, int NTW, int P, int WAVES>
+// fewer where more ran slower. ONE: queries of one tile only, where longer ones go to a
+// kernel of more tiles.
+template <int G, int NTW, int P, int WAVES, bool ONE = false>
 void run(Mx4FwdArgs a, hipStream_t stream)
 {
-    const bool split = a.ntq > NTW;
+    const bool split = !ONE && a.ntq > NTW;
     a.qpw = split ? 1 : NTW / a.ntq;
     a.log2_qslot = 5;
     a.nqb = (int32_t)pieces(a.Nq, a.qpw);
@@ -495,8 +496,13 @@ void run(Mx4FwdArgs a, hipStream_t stream)
     // (more query registers beside an argmax's would spill)
 #define MAXSIM_MX4_SPLIT(ARGMAX, FAST)                                                                                  \
     do {                                                                                                                \
-        if (split) hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, kSplit>), grid, block, 0, stream, a);      \
-        else hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, kWhole>), grid, block, 0, stream, a);           \
+        if constexpr (!ONE) {                                                                                           \
+            if (split) {                                                                                                \
+                hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, kSplit>), grid, block, 0, stream, a);         \
+                break;                                                                                                  \
+            }                                                                                                           \
+        }                                                                                                               \
+        hipLaunchKernelGGL((fwd_mx4_kernel<G, NTW, P, ARGMAX, FAST, kWhole>), grid, block, 0, stream, a);                \
     } while (0)
     if constexpr (NTW < 4 || (NTW == 4 && G < 4)) {
         if (a.argmax && fast) MAXSIM_MX4_SPLIT(true, true);

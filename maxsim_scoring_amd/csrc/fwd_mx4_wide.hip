@@ -13,14 +13,14 @@ void launch_fwd_mx4_wide(const Mx4FwdArgs& a, int n, hipStream_t stream)
     } else if (a.nb <= 16) {
         if (n >= 3 && !a.argmax) run<4, 4, 2, 8>(a, stream);
         else if (n >= 2) run<4, 2, 2, 8>(a, stream);
-        else run<4, 1, 2, 8>(a, stream);
+        else run<4, 1, 2, 8, true>(a, stream);
     } else if (a.nb <= 24) {
         if (n >= 3 && !a.argmax) run<6, 4, 2, 4>(a, stream);
         else if (n >= 2) run<6, 2, 2, 4>(a, stream);
-        else run<6, 1, 2, 8>(a, stream);
+        else run<6, 1, 2, 8, true>(a, stream);
     } else {
         if (n >= 2) run<8, 2, 2, 4>(a, stream);
-        else run<8, 1, 2, 4>(a, stream);
+        else run<8, 1, 2, 4, true>(a, stream);
     }
 }
 

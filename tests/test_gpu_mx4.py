@@ -608,7 +608,7 @@ def test_scores_of_several_queries_a_wave(ms, d, Nq, Lq, n):
 
 # Little work: as few tiles a wave as the query's length leaves.
 @pytest.mark.parametrize("Nq,Lq", [(1, 20), (2, 40), (1, 70), (1, 160), (2, 300), (2, 3), (3, 16)])
-@pytest.mark.parametrize("d", [128, 100, 256, 200, 384, 300, 512, 500, 768, 700, 1024, 1000])
+@pytest.mark.parametrize("d", [128, 100, 80, 256, 200, 384, 300, 512, 450, 768, 700, 1024, 1000, 900])
 def test_scores_of_little_work(ms, d, Nq, Lq):
     _check_many_scores(ms, Nq, Lq, 5, 40, d, d + Lq)
 
