@@ -13,7 +13,7 @@ from .binding import (MaxSimError, embed_tokens_i8, embed_tokens_mx4, maxsim_abi
                       maxsim_dropout_bwd, maxsim_dropout_fwd, maxsim_embed_i8, maxsim_fwd,
                       maxsim_fwd_i8, maxsim_fwd_i8_tok, maxsim_fwd_mx4, maxsim_fwd_pairs, maxsim_fwd_pairs_varlen,
                       maxsim_fwd_varlen, maxsim_linear_i8, maxsim_linear_mx4, maxsim_logprob_bwd,
-                      maxsim_logprob_fwd, maxsim_normalize_bwd,
+                      maxsim_logprob_fwd, maxsim_logprob_workspace, maxsim_normalize_bwd,
                       maxsim_normalize_fwd, maxsim_quantize_mx4, maxsim_quantize_tok, maxsim_status_string, maxsim_topk,
                       two_stage_topk, two_stage_topk_mx4)
 
@@ -25,5 +25,5 @@ __all__ = ["MaxSimError", "maxsim_fwd", "maxsim_fwd_varlen", "maxsim_fwd_i8", "m
            "maxsim_dropout_bwd",
            "maxsim_quantize_mx4", "maxsim_dequantize_mx4", "maxsim_linear_mx4", "maxsim_fwd_mx4",
            "embed_tokens_mx4", "two_stage_topk_mx4",
-           "maxsim_logprob_fwd", "maxsim_logprob_bwd",
+           "maxsim_logprob_fwd", "maxsim_logprob_bwd", "maxsim_logprob_workspace",
            "maxsim_status_string", "maxsim_abi_version"]

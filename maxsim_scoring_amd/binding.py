@@ -1011,6 +1011,15 @@ def _logprob_args(X, targets, mask):
     return code, X.shape[0], X.shape[1], targets.shape[1]
 
 
+def maxsim_logprob_workspace(Nq: int, Nd: int, P: int, k: int = 0) -> int:
+    """Bytes of workspace that maxsim_logprob_fwd needs for these sizes, 0 for rows of up
+    to 4096 columns. Calls that may run at the same time need one each."""
+    need = lib().maxsim_logprob_workspace(Nq, Nd, P, k)
+    if need < 0:
+        raise ValueError(f"sizes {Nq}, {Nd}, {P}, {k} are refused")
+    return need
+
+
 def maxsim_logprob_fwd(X: torch.Tensor, targets: torch.Tensor, mask: Optional[torch.Tensor] = None,
                        scale: float = 1.0, k: int = 0, logp: Optional[torch.Tensor] = None,
                        rank: Optional[torch.Tensor] = None, norm: Optional[torch.Tensor] = None,
@@ -1022,7 +1031,7 @@ def maxsim_logprob_fwd(X: torch.Tensor, targets: torch.Tensor, mask: Optional[to
     ``scale`` X (2^-64 to 2^64), rows of scores X [Nq, Nd] (fp16/bf16/fp32), mask uint8 [Nq, Nd].
     Returns (logp [Nq, P], rank int32 [Nq, P], norm [Nq, 2], entropy [Nq],
     top_idx int32 [Nq, k], top_logp [Nq, k]; the last two None with k = 0).
-    ``workspace`` is uint8 of maxsim_logprob_workspace bytes."""
+    ``workspace`` is uint8 of maxsim_logprob_workspace bytes (allocated if left out)."""
     code, Nq, Nd, P = _logprob_args(X, targets, mask)
     k = int(k)
     if not 0 <= k <= 1024:

@@ -157,6 +157,17 @@ def test_logprob_workspace(L):
         assert f(*bad) == -1, bad
 
 
+def test_binding_tells_the_workspace(L):
+    """The size that maxsim_logprob_fwd's documentation names is to be had without the C library."""
+    import maxsim_scoring_amd as ms
+    assert "maxsim_logprob_workspace" in ms.__all__
+    assert ms.maxsim_logprob_workspace(7, 4096, 5) == 0
+    assert ms.maxsim_logprob_workspace(7, 4097, 5, 8) == L.maxsim_logprob_workspace(7, 4097, 5, 8) > 0
+    for bad in ((7, -1, 5, 8), (7, 5000, 5, 1025), (1 << 31, 5, 1, 1)):
+        with pytest.raises(ValueError):
+            ms.maxsim_logprob_workspace(*bad)
+
+
 def test_logprob_largest_sizes(L):
     """The header's limit itself: 2^31 - 4097 is the largest size, 2^31 - 4096 is refused."""
     f, most = L.maxsim_logprob_workspace, (1 << 31) - 4097
