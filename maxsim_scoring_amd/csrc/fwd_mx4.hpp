@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
             // Sums of a finished document, tiles in order. Both halves of a wave hold the
             // maxima of 32 columns, over different rows: the halves of two tiles are swapped so
             // that one maximum joins both, the first tile's in the low half.
-            auto finish = [&](int doc) {
+            auto finish = [&](int doc) __attribute__((always_inline)) {
                 int i = i0, at = 0;  // the query of tile n, and which of its tiles that is
                 float sums = 0.0f;   // of this lane's columns of the query's tiles so far
                 auto put = [&](int n, int idx) {
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
             uint32_t words = 0;  // this lane's of 64 mask words of doc
             const uint8_t* codes = a.D + (int64_t)b0 * Ld * nb * 16;  // of the tile issued last
             const uint8_t* scales = a.d_scale + (int64_t)b0 * Ld * nb;
-            auto issue = [&](Slot& s) {
+            auto issue = [&](Slot& s) __attribute__((always_inline)) {
                 ++tile;
                 codes += 32 * 16 * nb;
                 scales += 32 * nb;
@@ -392,9 +392,9 @@ __global__ __launch_bounds__(kWaves * 64) void fwd_mx4_kernel(Mx4FwdArgs a)
                 s.bits = bits;
                 s.last = tile + 1 == count;
             };
-            auto consume = [&](Slot& s) {
+            auto consume = [&](Slot& s) __attribute__((always_inline)) {
                 place_scales<G, FAST>(s.t, h);
-                auto fold = [&](auto masked) {
+                auto fold = [&](auto masked) __attribute__((always_inline)) {
                     f32x16 start;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) start[e] = 0.0f;

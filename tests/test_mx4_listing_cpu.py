@@ -54,3 +54,15 @@ def test_a_result_that_some_lanes_use_is_computed_by_all(tmp_path):
     product = [k for k, i in enumerate(code) if i.startswith("v_mfma_scale")]
     narrowed = [k for k, i in enumerate(code) if re.match(r"s_\w*saveexec|s_\w+ exec,", i)]
     assert len(product) == 1 and narrowed and product[0] < narrowed[0]
+
+
+def test_kernels_call_no_functions():
+    """The parts of a kernel are inlined into it. In one that is called, what is uniform for
+    the kernel arrives in each lane's registers: its branches narrow EXEC, and what it takes
+    by reference lies in scratch memory."""
+    from maxsim_scoring_amd import binding
+    if not os.path.exists(binding.LIB_PATH):
+        build.build()
+    text = open(binding.LIB_PATH, "rb").read()
+    assert re.search(rb"_ZN6maxsim\w*fwd_mx4_kernel\w*", text)
+    assert not set(re.findall(rb"_ZZN6maxsim\w*_kernel\w*_cl\w*", text))
