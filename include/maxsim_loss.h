@@ -78,7 +78,10 @@ maxsim_status_t maxsim_logprob_fwd(maxsim_dtype_t dtype, const void* X, int64_t 
  *   X, scale, mask, targets, norm, entropy as in the forward and from it;
  *   grad_logp [Nq, P] float32; grad_entropy [Nq] float32, with entropy, or both
  *   NULL; dX [Nq, Nd] of `dx_dtype` (F16, BF16, F32): fully overwritten
- * Gradients of targets that are named more than once are added in the order of p.
+ * Gradients of targets that are named more than once are added in the order of p
+ * (for a column of probability above 0.6 in another order, a fixed one too). Such a
+ * column's dX is formed from 1 - p_c, which L holds to 32 bits beside a 2^-47 of the
+ * float64 sums, so that it does not lose the digits of a p_c next to 1.
  * Errors: SHAPE (negative sizes), UNSUPPORTED (dtypes, scale, alignment), NULL
  * (also one of entropy and grad_entropy without the other), OVERFLOW as above.
  */

@@ -92,7 +92,8 @@ maxsim_status_t maxsim_linear_mx4(maxsim_dtype_t dtype, const uint8_t* A, const 
  *   Q [Nq, Lq, d] and D [Nd, Ld, d] as codes and scales, 1 <= d <= 1024
  *   masks, scores [Nq, Nd] and argmax [Nq, Nd, Lq] (or NULL) as in maxsim_fwd
  * Similarities are sums in float32, as in the other forwards, so the argmax is
- * that of the rounded ones; ties among equal maxima go to the lowest index.
+ * that of the rounded ones; ties among equal maxima go to the lowest index (of the
+ * tokens that count, where all of them are at -Inf by products that overflow).
  * Masked tokens and rows are not looked at, whatever they hold. If a token that
  * counts holds a NaN block, the scores that it enters are NaN, and the argmax
  * is unspecified (in [0, Ld)).

@@ -8,10 +8,10 @@
 // columns in slots in the same way. The sums over a query's columns take two
 // documents at a time, and one store writes those of all documents of the tile. 3
 // queries of 5 tokens over 49,824 documents of 8 take 7.7 us (2.6 TB/s; a document a
-// tile 28.9), one query over 500,000 documents of 16 119 us (3.5 TB/s; 150). The
+// tile 28.9), one query over 500,000 documents of 16 110 us (3.8 TB/s; 150). The
 // instructions of a tile are the bound: exponents in aligned words were worth 199 to
 // 119 us there. Paths of their own for tiles without a masked row made it three times
-// the code for 42 queries over 9981 documents of 2 tokens in 13 instead of 16 us.
+// the code for 42 queries over 9981 documents of 2 tokens in 14 instead of 16 us.
 #include "fwd_mx4.hpp"
 
 namespace maxsim {
@@ -199,8 +199,8 @@ void run_short(Mx4FwdArgs a, hipStream_t stream)
 
 }  // namespace
 
-// 42 queries of 64 tokens over 9981 documents of 2 tokens take 16 us, 97 with a document
-// a tile; one query over 500,000 documents of 16 119 and 150. Where there is less than
+// 42 queries of 64 tokens over 9981 documents of 2 tokens take 15.4 us, 97 with a document
+// a tile; one query over 500,000 documents of 16 110 and 150. Where there is less than
 // a tile for each CU, a document a tile spreads further (10 queries of 48 tokens, 56
 // documents of one, 1024 channels: 9.3 us against 13.1), so this is refused (false).
 bool launch_fwd_mx4_short(Mx4FwdArgs a, hipStream_t stream)

@@ -4,7 +4,10 @@
 
 namespace maxsim {
 
-// n: query tiles a wave that leave work for all.
+// n: query tiles a wave that leave work for all. A width between the classes takes the
+// kernel above it: one query over 10,000 documents of 180 tokens 51.9 us at 384 channels,
+// 80 at 512, 138 at 640, 123 at 768, 268 at 896 and 149 at 1024 (exponents of whole words
+// only where all of a class's blocks are there).
 void launch_fwd_mx4_wide(const Mx4FwdArgs& a, int n, hipStream_t stream)
 {
     if (a.nb <= 12) {

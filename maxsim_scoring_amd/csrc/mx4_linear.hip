@@ -16,13 +16,13 @@
 // few_mx4_kernel: a few tokens. W is the traffic; fragments go straight from
 // memory to registers, 8 waves split k, and LDS joins their sums.
 //
-// 8192 x 4096 x 4096 to bf16 takes 80 us (3.4 PFLOP/s), 8192 x 8192 x 8192 270 us
-// (4.1), where a loop of these MFMAs alone reaches 4.6 to 5.1 on such values (power
-// is the limit; 7.5 on zeros): about 20 us go to filling the pipeline and to 67 MB of
-// outputs, the rest grows with k at 4.4 PFLOP/s. One token by 4096 x 4096: 5.0 us for
-// 8.9 MB, most of it the latency of a launch and of one chain of loads. Not faster
-// were tiles of 128 x 128 a wave (94 against 87 us at the time), workgroups that take
-// several 256 x 256 tiles, and outputs turned through LDS.
+// 8192 x 4096 x 4096 to bf16 takes 80 us (3.4 PFLOP/s; the profiler's median is 81 to
+// 84), 8192 x 8192 x 8192 270 us (4.1), where a loop of these MFMAs alone reaches 4.6
+// to 5.1 on such values (power is the limit; 7.5 on zeros): about 20 us go to filling
+// the pipeline and to 67 MB of outputs, the rest grows with k at 4.4 PFLOP/s. One token
+// by 4096 x 4096: 5.0 us for 8.9 MB, most of it the latency of a launch and of one chain
+// of loads. Not faster were tiles of 128 x 128 a wave (94 against 87 us at the time),
+// workgroups that take several 256 x 256 tiles, and outputs turned through LDS.
 #include "mx4_common.hpp"
 #include "kernels.hpp"
 
@@ -414,7 +414,10 @@ void run_few(const Mx4LinearArgs& a, hipStream_t stream)
 // 8192 x 8192 270 us), and 128 x 128 in workgroups that take many hides the outputs of
 // narrow products (360,000 x 768 to 128 channels: 48 us, with one tile a workgroup 66);
 // with fewer tiles than CUs 64 x 64 (1024 x 4096 x 4096 in 256 tiles of 128 18.6 us, in
-// 1024 of 64 23). Where even tiles of 32 x 16 leave CUs idle, their waves split k.
+// 1024 of 64 23; 512 x 4096 x 4096 16.1 and 12.9; 4096 x 4096 x 4096 in tiles of 256 42
+// and of 128 51). Where even tiles of 32 x 16 leave CUs idle, their waves split k (512 x
+// 128 x 768 4.06 us against 4.16 in 64 x 64); with more of them than CUs the weights are
+// read too often (48 x 4096 x 4096 12.5 against 8.1, 256 x 1024 x 1024 6.5 against 4.4).
 void linear_once(const Mx4LinearArgs& a, hipStream_t stream)
 {
     const int64_t cus = device_cu_count();
