@@ -783,7 +783,7 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
     __shared__ float add[Y::kColumns];  // the targets' gradients, by column
     __shared__ int cols[T];
     __shared__ float grads[T];
-    __shared__ float red[T / 64], red_a[T / 64];
+    __shared__ float red[2][T / 64];
 
     const int64_t unit = blockIdx.x, i = unit / a.chunks;
     const int c0 = (int)(unit % a.chunks) * Y::kColumns;
@@ -791,7 +791,7 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
     load_columns<E, T, N>(a, i, c0, x);
     for (int k = threadIdx.x; k < Y::kColumns; k += T) add[k] = 0.0f;
     const float m = a.norm_in[2 * i], L = a.norm_in[2 * i + 1];
-    float A = 0.0f, R = 0.0f;  // the gradients that name columns of score m, and the others
+    float G = 0.0f, R = 0.0f;  // the gradients, and those that name columns of another score than m
     for (int p0 = 0; p0 < a.P; p0 += T) {
         const int p = p0 + (int)threadIdx.x;
         float xt;
@@ -799,8 +799,8 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
         float g = 0.0f;
         if (xt != -__builtin_inff()) g = a.g_logp[i * a.P + p];
         else c = -1;
-        A += xt == m ? g : 0.0f;
-        R += xt == m ? 0.0f : g;
+        G += g;
+        if (xt != m) R += g;
         const int at = c >= c0 && c - c0 < Y::kColumns ? c - c0 : -1;
         __syncthreads();  // add is zeroed, the last targets are added
         cols[threadIdx.x] = at;
@@ -824,22 +824,27 @@ __global__ __launch_bounds__(T) void logprob_bwd_kernel(LogprobArgs a)
             }
         }
     }
-    A = wave_reduce(A, AddOp{});
-    R = wave_reduce(R, AddOp{});
-    put(red_a, A);
-    put(red, R);
+    // A column with p = exp(-L) above 0.6, the only one whose score is m: the difference of
+    // the gradients that name it, G - R, and p G loses the digits of 1 - p, (1 - p) G - R does
+    // not. It takes the place of the other in a row's only store, or is stored over it (512
+    // rows of 100,000 columns 78.3 -> 78.4 us, if all are such rows 81; chosen before each of
+    // the stores 85).
+    const bool peaked = L >= 0.0f && L < 0.5f;  // (-Inf: no candidates)
+    G = wave_reduce(G, AddOp{});
+    put(red[0], G);
+    if (peaked) {
+        R = wave_reduce(R, AddOp{});
+        put(red[1], R);
+    }
     __syncthreads();
-    A = joined(red_a, A, AddOp{});
-    R = joined(red, R, AddOp{});
-    const float G = A + R;
+    G = joined(red[0], G, AddOp{});
 
     const float gh = a.g_entropy ? a.g_entropy[i] : 0.0f, H = a.g_entropy ? a.entropy_in[i] : 0.0f;
-    // A column with p = exp(-L) above 0.6, the only one whose score is m: the difference of A
-    // and p (A + R) loses the digits of 1 - p, A (1 - p) - p R does not. It takes the place
-    // of the other in a row's only store, or is stored over it (512 rows of 100,000 columns
-    // 79 -> 80 us; chosen before each of the stores 85).
-    const bool peaked = L >= 0.0f && L < 0.5f;  // (-Inf: no candidates)
-    const float sure = a.scale * (one_minus_exp(L) * A - exp_neg(-L) * __builtin_fmaf(gh, H - L, R));
+    float sure = 0.0f;
+    if (peaked) {
+        R = joined(red[1], R, AddOp{});
+        sure = a.scale * (__builtin_fmaf(one_minus_exp(L), G, -R) - exp_neg(-L) * gh * (H - L));
+    }
     const int n = a.Nd - c0;
 #pragma unroll
     for (int g = 0; g < N / Y::V; ++g) {
